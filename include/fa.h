@@ -433,6 +433,160 @@ size_t fa_splitkv_e4m3_workspace_size(const fa_splitkv_e4m3_args* args, int32_t 
 fa_status fa_fwd_splitkv_e4m3(const fa_splitkv_e4m3_args* args, int32_t num_splits, void* workspace,
                               size_t workspace_bytes, int32_t* splits_used, void* stream);
 
+/*
+ * Filling a paged KV cache (no counterpart in the reference pages, whose KV-cache
+ * path starts from a filled cache: "ai-reference-codex: forward CUDA kernel",
+ * section 8).  The new tokens of sequence s are rows [cu_seqlens[s],
+ * cu_seqlens[s + 1]) of q / k / v (cu_seqlens NULL: total / b rows each, total a
+ * multiple of b); seqlens_k[s] counts the sequence's keys AFTER the append, so the
+ * same tensor serves the attention call that follows.  New token i of n goes to
+ *   position t = seqlens_k[s] - n + i,
+ *   page block_table[s * block_table_stride + t / page_size], row t % page_size,
+ * as in fa_kvcache_args.  A token whose position is negative is padding: neither
+ * stored nor rotated.  On the way K (and Q, written to q_out) is rotated by its
+ * position: with R = rotary_dim and the table's row c_i = cos_sin[t][i],
+ * s_i = cos_sin[t][R / 2 + i] (i < R / 2), the pair (x, y) = (dims i and i + R / 2),
+ * or dims 2i and 2i + 1 when interleaved, becomes
+ *   (x c_i - y s_i, y c_i + x s_i),
+ * in fp32, every product and sum rounded once, then rounded to `dtype`; dims
+ * >= R pass unchanged.  q_out may be q itself (same pointer and strides), and must
+ * not overlap it otherwise.  Rows of q_out and of the cache that no stored token
+ * owns are left as they were.
+ */
+typedef struct {
+  fa_dtype dtype;                 /* of q, k, v, q_out and the cache */
+  int32_t b;                      /* sequences (>= 1) */
+  int32_t total;                  /* rows of q / k / v (>= 0) */
+  int32_t hq, hkv, d;             /* hq = 0: no queries; d in {64, 128, 256} */
+  const void* q;                  /* device, [total, hq, d] */
+  void* q_out;                    /* device, [total, hq, d], written */
+  const void* k;                  /* device, [total, hkv, d] */
+  const void* v;                  /* device, [total, hkv, d] */
+  int64_t q_strides[2];           /* (row, head) in elements, multiples of 8 */
+  int64_t q_out_strides[2];
+  int64_t k_strides[2];
+  int64_t v_strides[2];
+  const int32_t* cu_seqlens;      /* device, [b + 1] prefix sums of the new tokens, or NULL */
+  const int32_t* seqlens_k;       /* device, [b] keys per sequence after the append */
+  const float* cos_sin;           /* device, fp32 [max_positions, rotary_dim], contiguous, 16-byte aligned */
+  int32_t rotary_dim;             /* 0 = no rotation; a multiple of 16 (interleaved: of 8), at most d */
+  int32_t max_positions;
+  int32_t interleaved;            /* 0 or 1 */
+  int32_t num_pages, page_size;   /* page_size: a multiple of 64 */
+  const int32_t* block_table;     /* device, [b, block_table_stride] page indices */
+  int32_t block_table_stride;
+  void* k_cache;                  /* fa_kv_append: device, [num_pages, page_size, hkv, d] */
+  void* v_cache;
+  int64_t k_cache_strides[3];     /* (page, row, head) in elements, multiples of 8 */
+  int64_t v_cache_strides[3];
+  void* cache;                    /* fa_kv_append_int4: device, [num_pages, hkv, fa_kvcache_int4_page_bytes] */
+  int64_t cache_strides[2];       /* (page, head) in bytes, multiples of 16 */
+  int32_t group;                  /* fa_kv_append_int4: dims per (scale, min) pair: 32, 64 or 128, at most d */
+} fa_kv_append_args;
+
+/*
+ * Append to a 16-bit paged cache (what fa_fwd_kvcache reads).  Prefix sums,
+ * lengths and the block table live on the device and are checked there: a token
+ * outside its block-table row, on a page outside [0, num_pages) or past the
+ * rotation table is not stored, and FA_ERR_DEVICE_ARG is recorded for the next
+ * fa_sync_status (as it is for prefix sums that decrease or leave [0, total]).
+ * Two sequences that share a page must not write the same row of it.
+ */
+fa_status fa_kv_append(const fa_kv_append_args* args, void* stream);
+
+/*
+ * Append to a 4-bit paged cache: each new (token, KV head) row x, rounded to
+ * `dtype` after its rotation, is held in groups of `group` dims as
+ *   min = the group's smallest value,
+ *   scale = (max - min) / 15 rounded to `dtype` (0 when below 2^-100),
+ *   code = round-to-nearest-even((x - min) / scale), at most 15 (0 when scale is 0),
+ * for the value min + scale * code.  Values must be finite.
+ * Layout, per page and KV head: page_size / 32 units of 32 keys, each
+ *   [K codes, 16 d bytes][V codes, 16 d][K pairs][V pairs],
+ * pairs (scale, min) of `dtype` as [32][d / group][2].  With J = min(d / 32, 4):
+ *   K: 32-bit word ((32 c + key) * 4 + t) * J + j holds dims 32 (J c + j) + 8 t + n
+ *      of the key, n = 0..7 in bits [4n, 4n + 4);
+ *   V: 32-bit word ((((key / 8) * d / 32 / J + c) * 8 + g) * 4 + key % 8 / 2) * J + j
+ *      holds dims 32 (J c + j) + 4 g + n, n = 0..3, of an even key in bits
+ *      [4n, 4n + 4) and of the key after it in bits [16 + 4n, 20 + 4n).
+ * Checks as for fa_kv_append.
+ */
+fa_status fa_kv_append_int4(const fa_kv_append_args* args, void* stream);
+
+/* Bytes of one page of one KV head of a 4-bit cache; 0 for an unsupported combination. */
+size_t fa_kvcache_int4_page_bytes(int32_t page_size, int32_t d, int32_t group);
+
+/*
+ * Read back from a 4-bit cache: rows [cu_seqlens[s], cu_seqlens[s + 1]) of k and v
+ * (cu_seqlens NULL: total / b rows each) become the last n_s keys and values of
+ * sequence s, min + scale * code rounded to `dtype`.  With n_s = seqlens_k[s] they
+ * are the sequence's whole cache: what a prompt's later chunk attends to through
+ * fa_fwd_varlen.  Rows of no sequence and of negative positions are left as they
+ * were; the checks are fa_kv_append's.
+ */
+typedef struct {
+  fa_dtype dtype;                 /* of the cache's pairs and of k, v */
+  int32_t b, total, hkv, d, group;
+  const void* cache;              /* as in fa_kv_append_args */
+  int64_t cache_strides[2];
+  int32_t num_pages, page_size;
+  const int32_t* block_table;
+  int32_t block_table_stride;
+  const int32_t* seqlens_k;       /* device, [b] keys per sequence */
+  const int32_t* cu_seqlens;      /* device, [b + 1], or NULL */
+  void* k;                        /* device, [total, hkv, d], written */
+  void* v;
+  int64_t k_strides[2];           /* (row, head) in elements, multiples of 8 */
+  int64_t v_strides[2];
+} fa_kv_gather_int4_args;
+
+fa_status fa_kv_gather_int4(const fa_kv_gather_int4_args* args, void* stream);
+
+/*
+ * Attention of sq query tokens per sequence over a 4-bit paged cache
+ * (fa_fwd_kvcache's counterpart; the values are those of fa_kv_append_int4, widened
+ * exactly).  Query i of sequence s stands at position t = seqlens_k[s] - sq + i and
+ * sees keys j <= t, with local = 1 only those j >= t - window_left; a query that sees
+ * no key (a negative position) gets O = 0, LSE = -inf.  Scores, softcap, softmax and
+ * LSE as in fa_fwd_args, statistics in fp32.  Made for few queries (decode, drafted
+ * tokens): every 16 rows (query tokens x query heads of a KV head) read the cache
+ * once; a long chunk goes through fa_kv_gather_int4 and fa_fwd_varlen.  The cache
+ * beyond a sequence's length is never used, whatever it holds.  Lengths and pages are
+ * checked on the device: a sequence longer than its block-table row, or a page
+ * outside [0, num_pages), is not read, FA_ERR_DEVICE_ARG is recorded and that
+ * sequence's O and LSE are undefined.
+ */
+typedef struct {
+  fa_dtype dtype;                 /* of q, o and the cache's pairs */
+  int32_t b, sq, hq, hkv, d;      /* hq % hkv == 0; d in {64, 128, 256}; b, sq, hq <= 65535 */
+  int32_t group;
+  const void* q;                  /* device, [b, sq, hq, d] */
+  int64_t q_strides[3];           /* (batch, row, head) in elements, multiples of 8 */
+  const void* cache;              /* as in fa_kv_append_args */
+  int64_t cache_strides[2];
+  int32_t num_pages, page_size;
+  const int32_t* block_table;
+  int32_t block_table_stride;
+  const int32_t* seqlens_k;       /* device, [b] keys per sequence, the query tokens' own among them */
+  void* o;                        /* device, [b, sq, hq, d], written */
+  int64_t o_strides[3];
+  float* lse;                     /* device, fp32 [b, hq, sq], contiguous, written */
+  float scale;                    /* finite, > 0 */
+  int32_t local;                  /* 0 or 1 */
+  int32_t window_left;            /* local: -1 = no left edge */
+  float softcap;                  /* 0 = off */
+} fa_kvcache_int4_args;
+
+/* Workspace bytes fa_fwd_kvcache_int4 needs on the current device; 0 if invalid. */
+size_t fa_kvcache_int4_workspace_size(const fa_kvcache_int4_args* args);
+
+/*
+ * Enqueue the attention.  The workspace is caller-owned device memory, 256-byte
+ * aligned, needing no initialisation; two calls whose work overlaps on the GPU need
+ * different workspaces.
+ */
+fa_status fa_fwd_kvcache_int4(const fa_kvcache_int4_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Size of the built-in split-KV scratch used by fa_fwd_splitkv_noalloc (per device). */
 #define FA_NOALLOC_SCRATCH_BYTES (8u << 20)
 

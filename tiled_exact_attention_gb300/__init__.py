@@ -8,11 +8,16 @@ from .api import (  # noqa: F401
     fa_bwd_workspace_size,
     fa_fwd,
     fa_fwd_kvcache,
+    fa_fwd_kvcache_int4,
     fa_fwd_splitkv,
     fa_fwd_e4m3,
     fa_fwd_splitkv_noalloc,
     fa_fwd_splitkv_e4m3,
     fa_fwd_varlen,
+    fa_kv_append,
+    fa_kv_append_int4,
+    fa_kv_gather_int4,
+    fa_kvcache_int4_page_bytes,
     fa_num_splits_heuristic,
     fa_quantize_e4m3,
     quantize_qkv_e4m3,

@@ -39,6 +39,12 @@ EXPORTS = (
     "fa_splitkv_e4m3_workspace_size",
     "fa_fwd_splitkv_e4m3",
     "fa_fwd_e4m3",
+    "fa_kv_append",
+    "fa_kv_append_int4",
+    "fa_kvcache_int4_page_bytes",
+    "fa_kv_gather_int4",
+    "fa_kvcache_int4_workspace_size",
+    "fa_fwd_kvcache_int4",
     "fa_splitkv_combine",
     "fa_sync_status",
     "fa_selftest_wait_timeout",
@@ -254,6 +260,99 @@ class SplitkvE4m3Args(ctypes.Structure):
     ]
 
 
+class KvAppendArgs(ctypes.Structure):
+    """Mirror of `fa_kv_append_args`."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int),
+        ("b", ctypes.c_int32),
+        ("total", ctypes.c_int32),
+        ("hq", ctypes.c_int32),
+        ("hkv", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("q", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("q_strides", ctypes.c_int64 * 2),
+        ("q_out_strides", ctypes.c_int64 * 2),
+        ("k_strides", ctypes.c_int64 * 2),
+        ("v_strides", ctypes.c_int64 * 2),
+        ("cu_seqlens", ctypes.c_void_p),
+        ("seqlens_k", ctypes.c_void_p),
+        ("cos_sin", ctypes.c_void_p),
+        ("rotary_dim", ctypes.c_int32),
+        ("max_positions", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("block_table", ctypes.c_void_p),
+        ("block_table_stride", ctypes.c_int32),
+        ("k_cache", ctypes.c_void_p),
+        ("v_cache", ctypes.c_void_p),
+        ("k_cache_strides", ctypes.c_int64 * 3),
+        ("v_cache_strides", ctypes.c_int64 * 3),
+        ("cache", ctypes.c_void_p),
+        ("cache_strides", ctypes.c_int64 * 2),
+        ("group", ctypes.c_int32),
+    ]
+
+
+class KvGatherInt4Args(ctypes.Structure):
+    """Mirror of `fa_kv_gather_int4_args`."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int),
+        ("b", ctypes.c_int32),
+        ("total", ctypes.c_int32),
+        ("hkv", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+        ("cache", ctypes.c_void_p),
+        ("cache_strides", ctypes.c_int64 * 2),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("block_table", ctypes.c_void_p),
+        ("block_table_stride", ctypes.c_int32),
+        ("seqlens_k", ctypes.c_void_p),
+        ("cu_seqlens", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_strides", ctypes.c_int64 * 2),
+        ("v_strides", ctypes.c_int64 * 2),
+    ]
+
+
+class KvcacheInt4Args(ctypes.Structure):
+    """Mirror of `fa_kvcache_int4_args`."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int),
+        ("b", ctypes.c_int32),
+        ("sq", ctypes.c_int32),
+        ("hq", ctypes.c_int32),
+        ("hkv", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+        ("q", ctypes.c_void_p),
+        ("q_strides", ctypes.c_int64 * 3),
+        ("cache", ctypes.c_void_p),
+        ("cache_strides", ctypes.c_int64 * 2),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("block_table", ctypes.c_void_p),
+        ("block_table_stride", ctypes.c_int32),
+        ("seqlens_k", ctypes.c_void_p),
+        ("o", ctypes.c_void_p),
+        ("o_strides", ctypes.c_int64 * 3),
+        ("lse", ctypes.c_void_p),
+        ("scale", ctypes.c_float),
+        ("local", ctypes.c_int32),
+        ("window_left", ctypes.c_int32),
+        ("softcap", ctypes.c_float),
+    ]
+
+
 class FaError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -309,6 +408,20 @@ def load():
         lib.fa_splitkv_e4m3_workspace_size.restype = ctypes.c_size_t
         lib.fa_fwd_splitkv_e4m3.argtypes = [pse, i32, vp, ctypes.c_size_t, ctypes.POINTER(i32), vp]
         lib.fa_fwd_splitkv_e4m3.restype = ctypes.c_int
+        pap = ctypes.POINTER(KvAppendArgs)
+        lib.fa_kv_append.argtypes = [pap, vp]
+        lib.fa_kv_append.restype = ctypes.c_int
+        lib.fa_kv_append_int4.argtypes = [pap, vp]
+        lib.fa_kv_append_int4.restype = ctypes.c_int
+        lib.fa_kvcache_int4_page_bytes.argtypes = [i32, i32, i32]
+        lib.fa_kvcache_int4_page_bytes.restype = ctypes.c_size_t
+        lib.fa_kv_gather_int4.argtypes = [ctypes.POINTER(KvGatherInt4Args), vp]
+        lib.fa_kv_gather_int4.restype = ctypes.c_int
+        pk4 = ctypes.POINTER(KvcacheInt4Args)
+        lib.fa_kvcache_int4_workspace_size.argtypes = [pk4]
+        lib.fa_kvcache_int4_workspace_size.restype = ctypes.c_size_t
+        lib.fa_fwd_kvcache_int4.argtypes = [pk4, vp, ctypes.c_size_t, vp]
+        lib.fa_fwd_kvcache_int4.restype = ctypes.c_int
         lib.fa_splitkv_combine.argtypes = [vp, vp, i32, i32, i32, i32, i32, ctypes.c_int, vp,
                                            ctypes.POINTER(i64), vp, vp]
         lib.fa_splitkv_combine.restype = ctypes.c_int

@@ -13,8 +13,8 @@ import math
 import torch
 
 from . import _lib
-from ._lib import (FA_BF16, FA_FP16, FA_OFFSET_BOTTOM_RIGHT, BwdArgs, E4m3Args, FwdArgs, KvcacheArgs, QuantArgs,
-                   SplitkvE4m3Args, VarlenArgs, check)
+from ._lib import (FA_BF16, FA_FP16, FA_OFFSET_BOTTOM_RIGHT, BwdArgs, E4m3Args, FwdArgs, KvAppendArgs, KvcacheArgs,
+                   KvcacheInt4Args, KvGatherInt4Args, QuantArgs, SplitkvE4m3Args, VarlenArgs, check)
 
 _DT = {torch.bfloat16: FA_BF16, torch.float16: FA_FP16}
 
@@ -455,6 +455,246 @@ def fa_fwd_splitkv_e4m3(q, k8, k_descale, v8, v_descale, *, scale=None, num_spli
                                   _stream_handle(stream)), "fa_fwd_splitkv_e4m3")
     if return_splits:
         return out, lse, int(used.value)
+    return out, lse
+
+
+def _on_device(device, stream, call):
+    """Run call(stream handle) with the tensors' device current (kernels launch on the current device)."""
+    if device.index == torch.cuda.current_device():
+        return call(_stream_handle(stream))
+    with torch.cuda.device(device):
+        return call(_stream_handle(stream))
+
+
+def _new_like(stream, device, *specs):
+    """Uninitialised tensors (shape, dtype) that belong to the stream the call runs on."""
+    if stream is None:
+        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
+    with torch.cuda.stream(stream):
+        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
+
+
+def _dense_strides(t: torch.Tensor):
+    """Strides of all but the last dimension; those of dimensions of one entry are never used and get a valid value."""
+    shape, st = t.shape, t.stride()
+    return tuple(st[i] if shape[i] > 1 else shape[-1] for i in range(len(shape) - 1))
+
+
+def _check_rows(device, dtype, **tensors):
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+            raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
+        if t.dtype != dtype or dtype not in _DT:
+            raise ValueError(f"{name} must be bf16 or fp16 like the others")
+        if t.stride(-1) != 1:
+            raise ValueError(f"{name} must have a contiguous head dimension")
+
+
+def _check_ints(device, **tensors):
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or t.stride(-1) != 1:
+            raise ValueError(f"{name} must be a CUDA int32 tensor on the device of the others, contiguous in its "
+                             "last dimension")
+
+
+def _fill_pages(a, block_table, seqlens_k, cu_seqlens, total):
+    """The block table, lengths and prefix sums of `fa_kv_append_args` / `fa_kv_gather_int4_args`."""
+    if block_table.dim() != 2 or seqlens_k.dim() != 1 or block_table.shape[0] != seqlens_k.shape[0]:
+        raise ValueError("block_table must be [b, n] and seqlens_k [b]")
+    a.b = seqlens_k.shape[0]
+    a.block_table = block_table.data_ptr()
+    a.block_table_stride = block_table.stride(0) if a.b > 1 else block_table.shape[1]
+    a.seqlens_k = seqlens_k.data_ptr()
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] != a.b + 1:
+            raise ValueError("cu_seqlens must hold b + 1 prefix sums")
+        a.cu_seqlens = cu_seqlens.data_ptr()
+    elif a.b == 0 or total % a.b:
+        raise ValueError("without cu_seqlens every sequence has the same number of rows")
+
+
+def _fill_cache4(a, cache, group, d):
+    """The 4-bit cache of an argument struct; its page size follows from the bytes of a page."""
+    if not isinstance(cache, torch.Tensor) or not cache.is_cuda or cache.dtype != torch.uint8 or cache.dim() != 3 \
+            or cache.stride(2) != 1:
+        raise ValueError("cache must be a CUDA uint8 [num_pages, hkv, page bytes] tensor, contiguous in its last "
+                         "dimension")
+    group = int(group)
+    if group not in (32, 64, 128) or group > d:
+        raise ValueError("group must be 32, 64 or 128 and at most the head dimension")
+    per_key = d + 8 * (d // group)
+    num_pages, hkv, size = cache.shape
+    if size == 0 or size % (64 * per_key):
+        raise ValueError(f"a page of one head holds a multiple of 64 keys of {per_key} bytes, not {size} bytes")
+    a.group = group
+    a.cache = cache.data_ptr()
+    a.cache_strides = (cache.stride(0) if num_pages > 1 else size * hkv, cache.stride(1) if hkv > 1 else size)
+    a.num_pages, a.page_size = num_pages, size // per_key
+
+
+def make_kv_append_args(k, v, *, block_table, seqlens_k, cu_seqlens=None, q=None, q_out=None, cos_sin=None,
+                        rotary_dim=None, interleaved: bool = False) -> KvAppendArgs:
+    """Fill the part of `fa_kv_append_args` that both caches share.  q, q_out: [total, hq, d]; k, v: [total, hkv, d];
+    cos_sin: fp32 [max_positions, rotary_dim], cosines then sines."""
+    _check_rows(k.device, k.dtype, k=k, v=v)
+    if k.dim() != 3 or v.shape != k.shape:
+        raise ValueError("k and v must both be [total, hkv, d]")
+    _check_ints(k.device, block_table=block_table, seqlens_k=seqlens_k, cu_seqlens=cu_seqlens)
+    total, hkv, d = k.shape
+    a = KvAppendArgs()
+    a.dtype, a.total, a.hkv, a.d = _DT[k.dtype], total, hkv, d
+    a.k, a.v = k.data_ptr(), v.data_ptr()
+    a.k_strides, a.v_strides = _dense_strides(k), _dense_strides(v)
+    _fill_pages(a, block_table, seqlens_k, cu_seqlens, total)
+    if q is not None:
+        _check_rows(k.device, k.dtype, q=q, q_out=q_out)
+        if q.dim() != 3 or q.shape[0] != total or q.shape[2] != d or q_out.shape != q.shape:
+            raise ValueError("q and q_out must both be [total, hq, d]")
+        a.hq, a.q, a.q_out = q.shape[1], q.data_ptr(), q_out.data_ptr()
+        a.q_strides, a.q_out_strides = _dense_strides(q), _dense_strides(q_out)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if cos_sin is not None:
+        if not isinstance(cos_sin, torch.Tensor) or cos_sin.device != k.device or cos_sin.dtype != torch.float32 \
+                or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous CUDA fp32 [max_positions, rotary_dim] tensor")
+        if rotary_dim is not None and rotary_dim != cos_sin.shape[1]:
+            raise ValueError("rotary_dim must be the width of cos_sin")
+        a.cos_sin, a.max_positions, a.rotary_dim = cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1]
+        a.interleaved = 1 if interleaved else 0
+    elif rotary_dim:
+        raise ValueError("a rotation needs cos_sin")
+    return a
+
+
+def fa_kv_append(k, v, k_cache, v_cache, *, block_table, seqlens_k, cu_seqlens=None, q=None, q_out=None, cos_sin=None,
+                 rotary_dim=None, interleaved: bool = False, stream=None):
+    """Append new keys and values [total, hkv, d] to a paged cache [num_pages, page_size, hkv, d], rotating k (and q)
+    by cos_sin at each token's position; returns the rotated q (None without q).  seqlens_k counts each sequence's
+    keys after the append; cu_seqlens None: the same number of new tokens for every sequence."""
+    if q is not None and q_out is None:
+        (q_out,) = _new_like(stream, k.device, (q.shape, q.dtype))
+    a = make_kv_append_args(k, v, block_table=block_table, seqlens_k=seqlens_k, cu_seqlens=cu_seqlens, q=q,
+                            q_out=q_out, cos_sin=cos_sin, rotary_dim=rotary_dim, interleaved=interleaved)
+    _check_rows(k.device, k.dtype, k_cache=k_cache, v_cache=v_cache)
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or k_cache.shape[2:] != k.shape[1:]:
+        raise ValueError("k_cache and v_cache must both be [num_pages, page_size, hkv, d]")
+    a.num_pages, a.page_size = k_cache.shape[0], k_cache.shape[1]
+    a.k_cache, a.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
+    a.k_cache_strides, a.v_cache_strides = _dense_strides(k_cache), _dense_strides(v_cache)
+    check(_on_device(k.device, stream, lambda s: _lib.load().fa_kv_append(ctypes.byref(a), s)), "fa_kv_append")
+    return q_out
+
+
+def fa_kv_append_int4(k, v, cache, *, group: int, block_table, seqlens_k, cu_seqlens=None, q=None, q_out=None,
+                      cos_sin=None, rotary_dim=None, interleaved: bool = False, stream=None):
+    """fa_kv_append into a 4-bit cache (uint8 [num_pages, hkv, fa_kvcache_int4_page_bytes(page_size, d, group)]): one
+    (scale, min) pair per token, head and group of `group` dims; returns the rotated q."""
+    if q is not None and q_out is None:
+        (q_out,) = _new_like(stream, k.device, (q.shape, q.dtype))
+    a = make_kv_append_args(k, v, block_table=block_table, seqlens_k=seqlens_k, cu_seqlens=cu_seqlens, q=q,
+                            q_out=q_out, cos_sin=cos_sin, rotary_dim=rotary_dim, interleaved=interleaved)
+    _fill_cache4(a, cache, group, k.shape[2])
+    if cache.device != k.device or cache.shape[1] != k.shape[1]:
+        raise ValueError("cache must hold k's heads, on k's device")
+    check(_on_device(k.device, stream, lambda s: _lib.load().fa_kv_append_int4(ctypes.byref(a), s)),
+          "fa_kv_append_int4")
+    return q_out
+
+
+def fa_kvcache_int4_page_bytes(page_size: int, d: int, group: int) -> int:
+    """Bytes of one page of one KV head of a 4-bit cache (0: unsupported)."""
+    return int(_lib.load().fa_kvcache_int4_page_bytes(int(page_size), int(d), int(group)))
+
+
+def fa_kv_gather_int4(cache, *, group: int, block_table, seqlens_k, cu_seqlens=None, k_out=None, v_out=None,
+                      total=None, d=None, dtype=None, stream=None):
+    """The last rows of each sequence of a 4-bit cache in 16 bits: sequence s fills rows [cu_seqlens[s],
+    cu_seqlens[s + 1]) of k_out and v_out [total, hkv, d] (cu_seqlens None: total / b rows each).  Without k_out
+    and v_out, total, d and dtype say what to allocate.  Returns (k_out, v_out)."""
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out come together")
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 3:
+        raise ValueError("cache must be [num_pages, hkv, page bytes]")
+    if k_out is None:
+        if total is None or d is None or dtype is None:
+            raise ValueError("total, d and dtype are needed to allocate the rows")
+        shape = (int(total), cache.shape[1], int(d))
+        k_out, v_out = _new_like(stream, cache.device, (shape, dtype), (shape, dtype))
+    _check_rows(cache.device, k_out.dtype, k_out=k_out, v_out=v_out)
+    if k_out.dim() != 3 or v_out.shape != k_out.shape or k_out.shape[1] != cache.shape[1]:
+        raise ValueError("k_out and v_out must both be [total, hkv, d]")
+    _check_ints(cache.device, block_table=block_table, seqlens_k=seqlens_k, cu_seqlens=cu_seqlens)
+    a = KvGatherInt4Args()
+    a.dtype = _DT[k_out.dtype]
+    a.total, a.hkv, a.d = k_out.shape
+    _fill_cache4(a, cache, group, a.d)
+    _fill_pages(a, block_table, seqlens_k, cu_seqlens, a.total)
+    a.k, a.v = k_out.data_ptr(), v_out.data_ptr()
+    a.k_strides, a.v_strides = _dense_strides(k_out), _dense_strides(v_out)
+    check(_on_device(cache.device, stream, lambda s: _lib.load().fa_kv_gather_int4(ctypes.byref(a), s)),
+          "fa_kv_gather_int4")
+    return k_out, v_out
+
+
+def make_kvcache_int4_args(q, cache, o, lse, *, group: int, block_table, seqlens_k, scale=None, window_left=None,
+                           softcap: float = 0.0) -> KvcacheInt4Args:
+    """Fill `fa_kvcache_int4_args`.  q, o: [b, sq, hq, d] (or [b, hq, d] for sq = 1); lse: fp32 [b, hq, sq]
+    ([b, hq])."""
+    _check_rows(cache.device, q.dtype, q=q, out=o)
+    one = q.dim() == 3
+    if q.dim() not in (3, 4) or o.shape != q.shape:
+        raise ValueError("q and out must both be [b, sq, hq, d] or [b, hq, d]")
+    b, sq, hq, d = (q.shape[0], 1, q.shape[1], q.shape[2]) if one else q.shape
+    if lse.shape != ((b, hq) if one else (b, hq, sq)) or lse.dtype != torch.float32 or lse.device != q.device \
+            or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 [b, hq, sq]")
+    _check_ints(q.device, block_table=block_table, seqlens_k=seqlens_k)
+    if block_table.dim() != 2 or block_table.shape[0] != b or seqlens_k.shape != (b,):
+        raise ValueError("block_table must be [b, n] and seqlens_k [b]")
+    a = KvcacheInt4Args()
+    a.dtype, a.b, a.sq, a.hq, a.hkv, a.d = _DT[q.dtype], b, sq, hq, cache.shape[1], d
+    _fill_cache4(a, cache, group, d)
+    a.q, a.o, a.lse = q.data_ptr(), o.data_ptr(), lse.data_ptr()
+    qs, os_ = _dense_strides(q), _dense_strides(o)
+    a.q_strides = (qs[0], d, qs[1]) if one else qs
+    a.o_strides = (os_[0], d, os_[1]) if one else os_
+    a.block_table = block_table.data_ptr()
+    a.block_table_stride = block_table.stride(0) if b > 1 else block_table.shape[1]
+    a.seqlens_k = seqlens_k.data_ptr()
+    a.scale = (1.0 / math.sqrt(d)) if scale is None else float(scale)
+    if window_left is not None:
+        a.local, a.window_left = 1, int(window_left)
+    a.softcap = float(softcap)
+    return a
+
+
+def fa_fwd_kvcache_int4(q, cache, *, group: int, block_table, seqlens_k, scale=None, window_left=None,
+                        softcap: float = 0.0, out=None, lse=None, workspace=None, stream=None):
+    """Attend the sq newest tokens of each sequence (q [b, sq, hq, d], or [b, hq, d]) to its 4-bit paged cache, each
+    token to the keys up to its own; returns (O like q, LSE [b, hq, sq] or [b, hq])."""
+    if not isinstance(q, torch.Tensor) or not isinstance(cache, torch.Tensor) or q.dim() not in (3, 4) \
+            or cache.dim() != 3:
+        raise ValueError("q must be [b, sq, hq, d] or [b, hq, d] and cache [num_pages, hkv, page bytes]")
+    if out is None:
+        (out,) = _new_like(stream, q.device, (q.shape, q.dtype))
+    if lse is None:
+        shape = q.shape[:2] if q.dim() == 3 else (q.shape[0], q.shape[2], q.shape[1])
+        (lse,) = _new_like(stream, q.device, (shape, torch.float32))
+    a = make_kvcache_int4_args(q, cache, out, lse, group=group, block_table=block_table, seqlens_k=seqlens_k,
+                               scale=scale, window_left=window_left, softcap=softcap)
+
+    def call(s):
+        ws, lib = workspace, _lib.load()
+        if ws is None:
+            need = int(lib.fa_kvcache_int4_workspace_size(ctypes.byref(a)))
+            (ws,) = _new_like(stream, q.device, ((max(need, 256),), torch.uint8))
+        return lib.fa_fwd_kvcache_int4(ctypes.byref(a), ctypes.c_void_p(ws.data_ptr()),
+                                       ws.numel() * ws.element_size(), s)
+
+    check(_on_device(q.device, stream, call), "fa_fwd_kvcache_int4")
     return out, lse
 
 

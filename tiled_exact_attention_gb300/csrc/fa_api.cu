@@ -10,6 +10,7 @@
 
 #include "fa.h"
 #include "fa_internal.h"
+#include "fa_kv4.h"
 #include "ptx.cuh"
 
 namespace fa {
@@ -417,6 +418,14 @@ int resolve_splits(const fa_fwd_args* a, int32_t requested, const DeviceInfo& di
 
 }  // namespace
 }  // namespace fa
+
+bool fa::current_device_info(int** status, int* sms) {
+  DeviceInfo di;
+  if (!device_info(&di)) return false;
+  *status = di.status;
+  *sms = di.sms;
+  return true;
+}
 
 using namespace fa;
 
