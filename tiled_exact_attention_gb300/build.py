@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfa.so")
 SOURCES = ["fa_api.cu", "fa_prefill.cu", "fa_decode.cu", "fa_backward.cu", "fa_fp8.cu", "fa_kv_api.cu",
-           "fa_kv_append.cu", "fa_attend4.cu"]
+           "fa_kv_append.cu", "fa_attend4_d64.cu", "fa_attend4_d128.cu", "fa_attend4_d256.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

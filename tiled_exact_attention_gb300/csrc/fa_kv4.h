@@ -88,6 +88,8 @@ struct Attend4Params {
   float* lse;     // [b][hq][sq]
   int64_t q_st[3], o_st[3];  // (batch, row, head) in elements
   int b, sq, hq, hkv, g, d, group;
+  int ntiles;     // row tiles of a KV head: ceil(sq * g / rows of a tile)
+  int grid;       // CTAs
   const uint8_t* cache;
   int64_t c_st[2];
   int num_pages, page_size;
@@ -97,12 +99,26 @@ struct Attend4Params {
   int window_left;   // -1: no left edge
   float scale_log2;  // scale * log2(e)
   float sc_k, sc_b;  // softcap as in DecodeParams (sc_b = 0: off)
+  // Partials of items that several CTAs share, two slots a CTA: O before the division
+  // [2 grid][rows][d], its maximum and sum [2 grid][rows]; counters [grid], zero at
+  // launch, one for the item that starts in a CTA's stretch and leaves it.
+  float* part_o;
+  float2* part_ml;
+  int* counters;
   int* status;
+};
+
+// The kernel a call takes: query rows of a tile, keys of a block, CTAs of a full grid.
+struct Attend4Plan {
+  int rows, block, max_ctas;
 };
 
 // dtype 0 = bf16, 1 = fp16.
 cudaError_t launch_kv_append(const KvAppendParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_kv_gather4(const KvGatherParams& p, int dtype, cudaStream_t stream);
-cudaError_t launch_attend4(const Attend4Params& p, int dtype, cudaStream_t stream);
+// With a plan: fill it from p.group, p.sq and p.g and launch nothing.
+cudaError_t attend4_d64(const Attend4Params& p, int dtype, int sms, Attend4Plan* plan, cudaStream_t stream);
+cudaError_t attend4_d128(const Attend4Params& p, int dtype, int sms, Attend4Plan* plan, cudaStream_t stream);
+cudaError_t attend4_d256(const Attend4Params& p, int dtype, int sms, Attend4Plan* plan, cudaStream_t stream);
 
 }  // namespace fa

@@ -144,6 +144,43 @@ fa_status validate_attend(const fa_kvcache_int4_args* a) {
   return FA_OK;
 }
 
+cudaError_t attend(const Attend4Params& p, int dtype, int sms, Attend4Plan* plan, cudaStream_t stream) {
+  if (p.d == 64) return attend4_d64(p, dtype, sms, plan, stream);
+  if (p.d == 128) return attend4_d128(p, dtype, sms, plan, stream);
+  return attend4_d256(p, dtype, sms, plan, stream);
+}
+
+size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// The kernel for a call, its grid and the sizes of its workspace's three parts.
+struct AttendWork {
+  Attend4Plan plan;
+  int ntiles, grid;
+  size_t o_bytes, ml_bytes, bytes;
+};
+
+bool plan_attend(const fa_kvcache_int4_args* a, int sms, AttendWork* w) {
+  Attend4Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.d = a->d;
+  p.group = a->group;
+  p.sq = a->sq;
+  p.g = a->hq / a->hkv;
+  if (attend(p, a->dtype, sms, &w->plan, nullptr) != cudaSuccess) return false;
+  const int64_t rows = static_cast<int64_t>(a->sq) * p.g;
+  w->ntiles = static_cast<int>((rows + w->plan.rows - 1) / w->plan.rows);
+  // no more CTAs than blocks there could be (a block table's row is the longest sequence)
+  const double blocks = static_cast<double>(a->b) * a->hkv * w->ntiles *
+                        (static_cast<double>(a->block_table_stride) * a->page_size / w->plan.block + 1.0);
+  w->grid = blocks < w->plan.max_ctas ? static_cast<int>(blocks) : w->plan.max_ctas;
+  if (w->grid < 1) w->grid = 1;
+  if (blocks / w->grid > 1e9) return false;  // (a CTA counts its blocks in 32 bits)
+  w->o_bytes = round256(static_cast<size_t>(2) * w->grid * w->plan.rows * a->d * sizeof(float));
+  w->ml_bytes = round256(static_cast<size_t>(2) * w->grid * w->plan.rows * sizeof(float2));
+  w->bytes = w->o_bytes + w->ml_bytes + round256(static_cast<size_t>(w->grid) * sizeof(int));
+  return true;
+}
+
 }  // namespace
 }  // namespace fa
 
@@ -201,7 +238,13 @@ fa_status fa_kv_gather_int4(const fa_kv_gather_int4_args* a, void* stream) {
 }
 
 size_t fa_kvcache_int4_workspace_size(const fa_kvcache_int4_args* a) {
-  return validate_attend(a) == FA_OK ? 256 : 0;
+  if (validate_attend(a) != FA_OK) return 0;
+  if (a->sq == 0) return 256;
+  int* status = nullptr;
+  int sms = 0;
+  AttendWork w;
+  if (!current_device_info(&status, &sms) || !plan_attend(a, sms, &w)) return 0;
+  return w.bytes;
 }
 
 fa_status fa_fwd_kvcache_int4(const fa_kvcache_int4_args* a, void* workspace, size_t workspace_bytes, void* stream) {
@@ -210,8 +253,16 @@ fa_status fa_fwd_kvcache_int4(const fa_kvcache_int4_args* a, void* workspace, si
   Attend4Params p;
   std::memset(&p, 0, sizeof(p));
   int sms = 0;
+  AttendWork w;
   if (!current_device_info(&p.status, &sms)) return FA_ERR_CUDA;
-  if (workspace == nullptr || workspace_bytes < 256 || !is_aligned(workspace, 256)) return FA_ERR_INVALID_ARG;
+  if (!plan_attend(a, sms, &w)) return FA_ERR_UNSUPPORTED;
+  if (workspace == nullptr || workspace_bytes < w.bytes || !is_aligned(workspace, 256)) return FA_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + w.o_bytes);
+  p.counters = reinterpret_cast<int*>(ws + w.o_bytes + w.ml_bytes);
+  p.ntiles = w.ntiles;
+  p.grid = w.grid;
   p.q = a->q;
   p.o = a->o;
   p.lse = a->lse;
@@ -241,7 +292,9 @@ fa_status fa_fwd_kvcache_int4(const fa_kvcache_int4_args* a, void* workspace, si
     p.sc_k = static_cast<float>(2.0 / static_cast<double>(a->softcap));
     p.sc_b = static_cast<float>(static_cast<double>(a->softcap) * 1.4426950408889634);
   }
-  return launch_attend4(p, a->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cudaMemsetAsync(p.counters, 0, static_cast<size_t>(w.grid) * sizeof(int), st) != cudaSuccess) return FA_ERR_CUDA;
+  return attend(p, a->dtype, sms, nullptr, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"
