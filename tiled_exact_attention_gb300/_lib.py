@@ -366,6 +366,8 @@ _lib = None
 def load():
     """Load libfa.so; raise if it has not been built (there is no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

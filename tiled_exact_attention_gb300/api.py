@@ -458,115 +458,147 @@ def fa_fwd_splitkv_e4m3(q, k8, k_descale, v8, v_descale, *, scale=None, num_spli
     return out, lse
 
 
-def _on_device(device, stream, call):
-    """Run call(stream handle) with the tensors' device current (kernels launch on the current device)."""
-    if device.index == torch.cuda.current_device():
-        return call(_stream_handle(stream))
+def _enqueue(fn, args, device: int, stream, *more):
+    """fn(args, *more, stream) with the tensors' device current (kernels launch on the current device)."""
+    if stream is not None:
+        raw = stream.cuda_stream
+    else:
+        raw = torch._C._cuda_getCurrentRawStream(device)
+    if device == torch.cuda.current_device():
+        return fn(ctypes.byref(args), *more, raw)
     with torch.cuda.device(device):
-        return call(_stream_handle(stream))
+        return fn(ctypes.byref(args), *more, raw)
 
 
-def _new_like(stream, device, *specs):
-    """Uninitialised tensors (shape, dtype) that belong to the stream the call runs on."""
+def _new(stream, device, shape, dtype):
+    """An uninitialised tensor that belongs to the stream the call runs on."""
     if stream is None:
-        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _dense_strides(t: torch.Tensor):
+def _dense_strides(t: torch.Tensor, shape):
     """Strides of all but the last dimension; those of dimensions of one entry are never used and get a valid value."""
-    shape, st = t.shape, t.stride()
-    return tuple(st[i] if shape[i] > 1 else shape[-1] for i in range(len(shape) - 1))
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError("every tensor must be contiguous in its last dimension")
+    if 1 in shape[:-1]:
+        return tuple(shape[-1] if n == 1 else x for n, x in zip(shape[:-1], st))
+    return st[:-1]
 
 
-def _check_rows(device, dtype, **tensors):
-    for name, t in tensors.items():
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
-            raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
-        if t.dtype != dtype or dtype not in _DT:
-            raise ValueError(f"{name} must be bf16 or fp16 like the others")
-        if t.stride(-1) != 1:
-            raise ValueError(f"{name} must have a contiguous head dimension")
+def _check_rows(device: int, dtype, *named):
+    for name, t in named:
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device:
+            raise ValueError(f"{name} must be a CUDA tensor of the type of the others, on their device")
 
 
-def _check_ints(device, **tensors):
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or t.stride(-1) != 1:
-            raise ValueError(f"{name} must be a CUDA int32 tensor on the device of the others, contiguous in its "
-                             "last dimension")
-
-
-def _fill_pages(a, block_table, seqlens_k, cu_seqlens, total):
-    """The block table, lengths and prefix sums of `fa_kv_append_args` / `fa_kv_gather_int4_args`."""
-    if block_table.dim() != 2 or seqlens_k.dim() != 1 or block_table.shape[0] != seqlens_k.shape[0]:
+def _pages(device: int, block_table, seqlens_k):
+    """(sequences, block table, its row stride, lengths) of a paged cache."""
+    if not isinstance(block_table, torch.Tensor) or not isinstance(seqlens_k, torch.Tensor) \
+            or block_table.dtype is not torch.int32 or seqlens_k.dtype is not torch.int32 \
+            or block_table.get_device() != device or seqlens_k.get_device() != device:
+        raise ValueError("block_table and seqlens_k must be CUDA int32 tensors on the device of the others")
+    if block_table.dim() != 2 or seqlens_k.dim() != 1:
         raise ValueError("block_table must be [b, n] and seqlens_k [b]")
-    a.b = seqlens_k.shape[0]
-    a.block_table = block_table.data_ptr()
-    a.block_table_stride = block_table.stride(0) if a.b > 1 else block_table.shape[1]
-    a.seqlens_k = seqlens_k.data_ptr()
-    if cu_seqlens is not None:
-        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] != a.b + 1:
-            raise ValueError("cu_seqlens must hold b + 1 prefix sums")
-        a.cu_seqlens = cu_seqlens.data_ptr()
-    elif a.b == 0 or total % a.b:
-        raise ValueError("without cu_seqlens every sequence has the same number of rows")
+    b, width = block_table.shape
+    if seqlens_k.shape[0] != b:
+        raise ValueError("block_table must be [b, n] and seqlens_k [b]")
+    row, col = block_table.stride()
+    if (col != 1 and width > 1) or (b > 1 and seqlens_k.stride(0) != 1):
+        raise ValueError("block_table must be contiguous in its last dimension, seqlens_k contiguous")
+    return b, block_table.data_ptr(), row if b > 1 else width, seqlens_k.data_ptr()
 
 
-def _fill_cache4(a, cache, group, d):
-    """The 4-bit cache of an argument struct; its page size follows from the bytes of a page."""
-    if not isinstance(cache, torch.Tensor) or not cache.is_cuda or cache.dtype != torch.uint8 or cache.dim() != 3 \
-            or cache.stride(2) != 1:
-        raise ValueError("cache must be a CUDA uint8 [num_pages, hkv, page bytes] tensor, contiguous in its last "
-                         "dimension")
-    group = int(group)
+def _prefix(device: int, cu_seqlens, b: int, total: int):
+    """Pointer of the prefix sums, None where every sequence has the same number of rows."""
+    if cu_seqlens is None:
+        if b == 0 or total % b:
+            raise ValueError("without cu_seqlens every sequence has the same number of rows")
+        return None
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dtype is not torch.int32 \
+            or cu_seqlens.get_device() != device or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] != b + 1 \
+            or cu_seqlens.stride(0) != 1:
+        raise ValueError("cu_seqlens must be a contiguous CUDA int32 vector of b + 1 prefix sums, on the device of "
+                         "the others")
+    return cu_seqlens.data_ptr()
+
+
+def _cache4(device: int, cache, group: int, d: int, hkv):
+    """(pointer, (page, head) strides, pages, page size, KV heads) of a 4-bit cache; the page size follows from the
+    bytes of a page."""
+    if not isinstance(cache, torch.Tensor) or cache.dtype is not torch.uint8 or cache.get_device() != device \
+            or cache.dim() != 3:
+        raise ValueError("cache must be a CUDA uint8 [num_pages, hkv, page bytes] tensor on the device of the others")
     if group not in (32, 64, 128) or group > d:
         raise ValueError("group must be 32, 64 or 128 and at most the head dimension")
     per_key = d + 8 * (d // group)
-    num_pages, hkv, size = cache.shape
+    pages, heads, size = cache.shape
+    if hkv is not None and heads != hkv:
+        raise ValueError("cache must hold the KV heads of the others")
     if size == 0 or size % (64 * per_key):
         raise ValueError(f"a page of one head holds a multiple of 64 keys of {per_key} bytes, not {size} bytes")
-    a.group = group
-    a.cache = cache.data_ptr()
-    a.cache_strides = (cache.stride(0) if num_pages > 1 else size * hkv, cache.stride(1) if hkv > 1 else size)
-    a.num_pages, a.page_size = num_pages, size // per_key
+    sp, sh, last = cache.stride()
+    if last != 1:
+        raise ValueError("cache must be contiguous in its last dimension")
+    return (cache.data_ptr(), (sp if pages > 1 else size * heads, sh if heads > 1 else size), pages, size // per_key,
+            heads)
 
 
-def make_kv_append_args(k, v, *, block_table, seqlens_k, cu_seqlens=None, q=None, q_out=None, cos_sin=None,
-                        rotary_dim=None, interleaved: bool = False) -> KvAppendArgs:
-    """Fill the part of `fa_kv_append_args` that both caches share.  q, q_out: [total, hq, d]; k, v: [total, hkv, d];
-    cos_sin: fp32 [max_positions, rotary_dim], cosines then sines."""
-    _check_rows(k.device, k.dtype, k=k, v=v)
-    if k.dim() != 3 or v.shape != k.shape:
+_NO2, _NO3 = (0, 0), (0, 0, 0)
+
+
+def _make_append_args(device: int, k, v, block_table, seqlens_k, cu_seqlens, q, q_out, cos_sin, rotary_dim, interleaved,
+                      k_cache=None, v_cache=None, cache=None, group=0) -> KvAppendArgs:
+    """`fa_kv_append_args` of either cache.  q, q_out: [total, hq, d]; k, v: [total, hkv, d]; cos_sin: fp32
+    [max_positions, rotary_dim], cosines then sines."""
+    dtype = k.dtype
+    if device < 0 or dtype not in _DT:
+        raise ValueError("k must be a CUDA bf16 or fp16 tensor")
+    _check_rows(device, dtype, ("v", v))
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape:
         raise ValueError("k and v must both be [total, hkv, d]")
-    _check_ints(k.device, block_table=block_table, seqlens_k=seqlens_k, cu_seqlens=cu_seqlens)
-    total, hkv, d = k.shape
-    a = KvAppendArgs()
-    a.dtype, a.total, a.hkv, a.d = _DT[k.dtype], total, hkv, d
-    a.k, a.v = k.data_ptr(), v.data_ptr()
-    a.k_strides, a.v_strides = _dense_strides(k), _dense_strides(v)
-    _fill_pages(a, block_table, seqlens_k, cu_seqlens, total)
+    total, hkv, d = shape
+    b, table, row, lens = _pages(device, block_table, seqlens_k)
+    cu = _prefix(device, cu_seqlens, b, total)
+    hq, q_at, qo_at, q_st, qo_st = 0, None, None, _NO2, _NO2
     if q is not None:
-        _check_rows(k.device, k.dtype, q=q, q_out=q_out)
-        if q.dim() != 3 or q.shape[0] != total or q.shape[2] != d or q_out.shape != q.shape:
+        _check_rows(device, dtype, ("q", q), ("q_out", q_out))
+        qs = q.shape
+        if len(qs) != 3 or qs[0] != total or qs[2] != d or q_out.shape != qs:
             raise ValueError("q and q_out must both be [total, hq, d]")
-        a.hq, a.q, a.q_out = q.shape[1], q.data_ptr(), q_out.data_ptr()
-        a.q_strides, a.q_out_strides = _dense_strides(q), _dense_strides(q_out)
+        hq, q_at, qo_at = qs[1], q.data_ptr(), q_out.data_ptr()
+        q_st, qo_st = _dense_strides(q, qs), _dense_strides(q_out, qs)
     elif q_out is not None:
         raise ValueError("q_out without q")
+    cs_at, rot, positions = None, 0, 0
     if cos_sin is not None:
-        if not isinstance(cos_sin, torch.Tensor) or cos_sin.device != k.device or cos_sin.dtype != torch.float32 \
-                or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        if not isinstance(cos_sin, torch.Tensor) or cos_sin.dtype is not torch.float32 \
+                or cos_sin.get_device() != device or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
             raise ValueError("cos_sin must be a contiguous CUDA fp32 [max_positions, rotary_dim] tensor")
-        if rotary_dim is not None and rotary_dim != cos_sin.shape[1]:
+        cs_at = cos_sin.data_ptr()
+        positions, rot = cos_sin.shape
+        if rotary_dim is not None and rotary_dim != rot:
             raise ValueError("rotary_dim must be the width of cos_sin")
-        a.cos_sin, a.max_positions, a.rotary_dim = cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1]
-        a.interleaved = 1 if interleaved else 0
     elif rotary_dim:
         raise ValueError("a rotation needs cos_sin")
-    return a
+    kc_at, vc_at, kc_st, vc_st, c_at, c_st = None, None, _NO3, _NO3, None, _NO2
+    if cache is None:
+        _check_rows(device, dtype, ("k_cache", k_cache), ("v_cache", v_cache))
+        cs = k_cache.shape
+        if len(cs) != 4 or v_cache.shape != cs or cs[2] != hkv or cs[3] != d:
+            raise ValueError("k_cache and v_cache must both be [num_pages, page_size, hkv, d]")
+        pages, page_size = cs[0], cs[1]
+        kc_at, vc_at = k_cache.data_ptr(), v_cache.data_ptr()
+        kc_st, vc_st = _dense_strides(k_cache, cs), _dense_strides(v_cache, cs)
+    else:
+        c_at, c_st, pages, page_size, _ = _cache4(device, cache, group, d, hkv)
+    return KvAppendArgs(_DT[dtype], b, total, hq, hkv, d, q_at, qo_at, k.data_ptr(), v.data_ptr(), q_st, qo_st,
+                        _dense_strides(k, shape), _dense_strides(v, shape), cu, lens, cs_at, rot, positions,
+                        1 if interleaved else 0, pages, page_size, table, row, kc_at, vc_at, kc_st, vc_st, c_at, c_st,
+                        group)
 
 
 def fa_kv_append(k, v, k_cache, v_cache, *, block_table, seqlens_k, cu_seqlens=None, q=None, q_out=None, cos_sin=None,
@@ -574,17 +606,12 @@ def fa_kv_append(k, v, k_cache, v_cache, *, block_table, seqlens_k, cu_seqlens=N
     """Append new keys and values [total, hkv, d] to a paged cache [num_pages, page_size, hkv, d], rotating k (and q)
     by cos_sin at each token's position; returns the rotated q (None without q).  seqlens_k counts each sequence's
     keys after the append; cu_seqlens None: the same number of new tokens for every sequence."""
-    if q is not None and q_out is None:
-        (q_out,) = _new_like(stream, k.device, (q.shape, q.dtype))
-    a = make_kv_append_args(k, v, block_table=block_table, seqlens_k=seqlens_k, cu_seqlens=cu_seqlens, q=q,
-                            q_out=q_out, cos_sin=cos_sin, rotary_dim=rotary_dim, interleaved=interleaved)
-    _check_rows(k.device, k.dtype, k_cache=k_cache, v_cache=v_cache)
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or k_cache.shape[2:] != k.shape[1:]:
-        raise ValueError("k_cache and v_cache must both be [num_pages, page_size, hkv, d]")
-    a.num_pages, a.page_size = k_cache.shape[0], k_cache.shape[1]
-    a.k_cache, a.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
-    a.k_cache_strides, a.v_cache_strides = _dense_strides(k_cache), _dense_strides(v_cache)
-    check(_on_device(k.device, stream, lambda s: _lib.load().fa_kv_append(ctypes.byref(a), s)), "fa_kv_append")
+    device = k.get_device()
+    if q is not None and q_out is None and device >= 0:
+        q_out = _new(stream, k.device, q.shape, q.dtype)
+    a = _make_append_args(device, k, v, block_table, seqlens_k, cu_seqlens, q, q_out, cos_sin, rotary_dim, interleaved,
+                          k_cache, v_cache)
+    check(_enqueue(_lib.load().fa_kv_append, a, device, stream), "fa_kv_append")
     return q_out
 
 
@@ -592,15 +619,14 @@ def fa_kv_append_int4(k, v, cache, *, group: int, block_table, seqlens_k, cu_seq
                       cos_sin=None, rotary_dim=None, interleaved: bool = False, stream=None):
     """fa_kv_append into a 4-bit cache (uint8 [num_pages, hkv, fa_kvcache_int4_page_bytes(page_size, d, group)]): one
     (scale, min) pair per token, head and group of `group` dims; returns the rotated q."""
-    if q is not None and q_out is None:
-        (q_out,) = _new_like(stream, k.device, (q.shape, q.dtype))
-    a = make_kv_append_args(k, v, block_table=block_table, seqlens_k=seqlens_k, cu_seqlens=cu_seqlens, q=q,
-                            q_out=q_out, cos_sin=cos_sin, rotary_dim=rotary_dim, interleaved=interleaved)
-    _fill_cache4(a, cache, group, k.shape[2])
-    if cache.device != k.device or cache.shape[1] != k.shape[1]:
-        raise ValueError("cache must hold k's heads, on k's device")
-    check(_on_device(k.device, stream, lambda s: _lib.load().fa_kv_append_int4(ctypes.byref(a), s)),
-          "fa_kv_append_int4")
+    device = k.get_device()
+    if cache is None:
+        raise ValueError("a 4-bit cache is needed")
+    if q is not None and q_out is None and device >= 0:
+        q_out = _new(stream, k.device, q.shape, q.dtype)
+    a = _make_append_args(device, k, v, block_table, seqlens_k, cu_seqlens, q, q_out, cos_sin, rotary_dim, interleaved,
+                          cache=cache, group=group)
+    check(_enqueue(_lib.load().fa_kv_append_int4, a, device, stream), "fa_kv_append_int4")
     return q_out
 
 
@@ -614,87 +640,72 @@ def fa_kv_gather_int4(cache, *, group: int, block_table, seqlens_k, cu_seqlens=N
     """The last rows of each sequence of a 4-bit cache in 16 bits: sequence s fills rows [cu_seqlens[s],
     cu_seqlens[s + 1]) of k_out and v_out [total, hkv, d] (cu_seqlens None: total / b rows each).  Without k_out
     and v_out, total, d and dtype say what to allocate.  Returns (k_out, v_out)."""
+    device = cache.get_device()
     if (k_out is None) != (v_out is None):
         raise ValueError("k_out and v_out come together")
-    if not isinstance(cache, torch.Tensor) or cache.dim() != 3:
-        raise ValueError("cache must be [num_pages, hkv, page bytes]")
+    if device < 0 or cache.dim() != 3:
+        raise ValueError("cache must be a CUDA [num_pages, hkv, page bytes] tensor")
     if k_out is None:
         if total is None or d is None or dtype is None:
             raise ValueError("total, d and dtype are needed to allocate the rows")
         shape = (int(total), cache.shape[1], int(d))
-        k_out, v_out = _new_like(stream, cache.device, (shape, dtype), (shape, dtype))
-    _check_rows(cache.device, k_out.dtype, k_out=k_out, v_out=v_out)
-    if k_out.dim() != 3 or v_out.shape != k_out.shape or k_out.shape[1] != cache.shape[1]:
-        raise ValueError("k_out and v_out must both be [total, hkv, d]")
-    _check_ints(cache.device, block_table=block_table, seqlens_k=seqlens_k, cu_seqlens=cu_seqlens)
-    a = KvGatherInt4Args()
-    a.dtype = _DT[k_out.dtype]
-    a.total, a.hkv, a.d = k_out.shape
-    _fill_cache4(a, cache, group, a.d)
-    _fill_pages(a, block_table, seqlens_k, cu_seqlens, a.total)
-    a.k, a.v = k_out.data_ptr(), v_out.data_ptr()
-    a.k_strides, a.v_strides = _dense_strides(k_out), _dense_strides(v_out)
-    check(_on_device(cache.device, stream, lambda s: _lib.load().fa_kv_gather_int4(ctypes.byref(a), s)),
-          "fa_kv_gather_int4")
+        k_out, v_out = _new(stream, cache.device, shape, dtype), _new(stream, cache.device, shape, dtype)
+    dtype, shape = k_out.dtype, k_out.shape
+    _check_rows(device, dtype, ("k_out", k_out), ("v_out", v_out))
+    if dtype not in _DT or len(shape) != 3 or v_out.shape != shape:
+        raise ValueError("k_out and v_out must both be bf16 or fp16 [total, hkv, d]")
+    total, hkv, d = shape
+    b, table, row, lens = _pages(device, block_table, seqlens_k)
+    cu = _prefix(device, cu_seqlens, b, total)
+    c_at, c_st, pages, page_size, _ = _cache4(device, cache, group, d, hkv)
+    a = KvGatherInt4Args(_DT[dtype], b, total, hkv, d, group, c_at, c_st, pages, page_size, table, row, lens, cu,
+                         k_out.data_ptr(), v_out.data_ptr(), _dense_strides(k_out, shape), _dense_strides(v_out, shape))
+    check(_enqueue(_lib.load().fa_kv_gather_int4, a, device, stream), "fa_kv_gather_int4")
     return k_out, v_out
-
-
-def make_kvcache_int4_args(q, cache, o, lse, *, group: int, block_table, seqlens_k, scale=None, window_left=None,
-                           softcap: float = 0.0) -> KvcacheInt4Args:
-    """Fill `fa_kvcache_int4_args`.  q, o: [b, sq, hq, d] (or [b, hq, d] for sq = 1); lse: fp32 [b, hq, sq]
-    ([b, hq])."""
-    _check_rows(cache.device, q.dtype, q=q, out=o)
-    one = q.dim() == 3
-    if q.dim() not in (3, 4) or o.shape != q.shape:
-        raise ValueError("q and out must both be [b, sq, hq, d] or [b, hq, d]")
-    b, sq, hq, d = (q.shape[0], 1, q.shape[1], q.shape[2]) if one else q.shape
-    if lse.shape != ((b, hq) if one else (b, hq, sq)) or lse.dtype != torch.float32 or lse.device != q.device \
-            or not lse.is_contiguous():
-        raise ValueError("lse must be contiguous fp32 [b, hq, sq]")
-    _check_ints(q.device, block_table=block_table, seqlens_k=seqlens_k)
-    if block_table.dim() != 2 or block_table.shape[0] != b or seqlens_k.shape != (b,):
-        raise ValueError("block_table must be [b, n] and seqlens_k [b]")
-    a = KvcacheInt4Args()
-    a.dtype, a.b, a.sq, a.hq, a.hkv, a.d = _DT[q.dtype], b, sq, hq, cache.shape[1], d
-    _fill_cache4(a, cache, group, d)
-    a.q, a.o, a.lse = q.data_ptr(), o.data_ptr(), lse.data_ptr()
-    qs, os_ = _dense_strides(q), _dense_strides(o)
-    a.q_strides = (qs[0], d, qs[1]) if one else qs
-    a.o_strides = (os_[0], d, os_[1]) if one else os_
-    a.block_table = block_table.data_ptr()
-    a.block_table_stride = block_table.stride(0) if b > 1 else block_table.shape[1]
-    a.seqlens_k = seqlens_k.data_ptr()
-    a.scale = (1.0 / math.sqrt(d)) if scale is None else float(scale)
-    if window_left is not None:
-        a.local, a.window_left = 1, int(window_left)
-    a.softcap = float(softcap)
-    return a
 
 
 def fa_fwd_kvcache_int4(q, cache, *, group: int, block_table, seqlens_k, scale=None, window_left=None,
                         softcap: float = 0.0, out=None, lse=None, workspace=None, stream=None):
     """Attend the sq newest tokens of each sequence (q [b, sq, hq, d], or [b, hq, d]) to its 4-bit paged cache, each
     token to the keys up to its own; returns (O like q, LSE [b, hq, sq] or [b, hq])."""
-    if not isinstance(q, torch.Tensor) or not isinstance(cache, torch.Tensor) or q.dim() not in (3, 4) \
-            or cache.dim() != 3:
-        raise ValueError("q must be [b, sq, hq, d] or [b, hq, d] and cache [num_pages, hkv, page bytes]")
+    device, shape, dtype = q.get_device(), q.shape, q.dtype
+    if device < 0 or dtype not in _DT or len(shape) not in (3, 4):
+        raise ValueError("q must be a CUDA bf16 or fp16 tensor [b, sq, hq, d] or [b, hq, d]")
+    if len(shape) == 4:
+        b, sq, hq, d = shape
+        lse_shape = (b, hq, sq)
+    else:
+        b, hq, d = lse_shape = shape
+        sq, lse_shape = 1, (b, hq)
     if out is None:
-        (out,) = _new_like(stream, q.device, (q.shape, q.dtype))
+        out = _new(stream, q.device, shape, dtype)
+    else:
+        _check_rows(device, dtype, ("out", out))
+        if out.shape != shape:
+            raise ValueError("out must be shaped like q")
     if lse is None:
-        shape = q.shape[:2] if q.dim() == 3 else (q.shape[0], q.shape[2], q.shape[1])
-        (lse,) = _new_like(stream, q.device, (shape, torch.float32))
-    a = make_kvcache_int4_args(q, cache, out, lse, group=group, block_table=block_table, seqlens_k=seqlens_k,
-                               scale=scale, window_left=window_left, softcap=softcap)
-
-    def call(s):
-        ws, lib = workspace, _lib.load()
-        if ws is None:
-            need = int(lib.fa_kvcache_int4_workspace_size(ctypes.byref(a)))
-            (ws,) = _new_like(stream, q.device, ((max(need, 256),), torch.uint8))
-        return lib.fa_fwd_kvcache_int4(ctypes.byref(a), ctypes.c_void_p(ws.data_ptr()),
-                                       ws.numel() * ws.element_size(), s)
-
-    check(_on_device(q.device, stream, call), "fa_fwd_kvcache_int4")
+        lse = _new(stream, q.device, lse_shape, torch.float32)
+    elif lse.shape != lse_shape or lse.dtype is not torch.float32 or lse.get_device() != device \
+            or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous CUDA fp32 [b, hq, sq] (or [b, hq])")
+    seqs, table, row, lens = _pages(device, block_table, seqlens_k)
+    if seqs != b:
+        raise ValueError("block_table must be [b, n] and seqlens_k [b]")
+    c_at, c_st, pages, page_size, hkv = _cache4(device, cache, group, d, None)
+    q_st, o_st = _dense_strides(q, shape), _dense_strides(out, shape)
+    if len(shape) == 3:
+        q_st, o_st = (q_st[0], d, q_st[1]), (o_st[0], d, o_st[1])
+    a = KvcacheInt4Args(_DT[dtype], b, sq, hq, hkv, d, group, q.data_ptr(), q_st, c_at, c_st, pages, page_size, table,
+                        row, lens, out.data_ptr(), o_st, lse.data_ptr(), d ** -0.5 if scale is None else scale,
+                        0 if window_left is None else 1, 0 if window_left is None else window_left, softcap)
+    lib = _lib.load()
+    if workspace is None:
+        need = _enqueue(lambda args, s: lib.fa_kvcache_int4_workspace_size(args), a, device, stream)
+        workspace = _new(stream, q.device, (max(int(need), 256),), torch.uint8)
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
+    check(_enqueue(lib.fa_fwd_kvcache_int4, a, device, stream, workspace.data_ptr(),
+                   workspace.numel() * workspace.element_size()), "fa_fwd_kvcache_int4")
     return out, lse
 
 
