@@ -45,16 +45,26 @@ enum : int { kSiteFull = 48 };
 
 template <int D, int NG, int NT>
 struct Cfg {
-  static constexpr int UNITS = D == 64 ? 2 : 1;  // units per block (a block lies in one page)
+#ifndef A4_UNITS
+#define A4_UNITS (D == 64 ? 2 : 1)
+#endif
+#ifndef A4_STAGES
+#define A4_STAGES (D == 256 ? 2 : 3)
+#endif
+#ifndef A4_CTAS
+#define A4_CTAS (SMEM <= 74 * 1024 ? 3 : (SMEM <= 112 * 1024 ? 2 : 1))
+#endif
+  static constexpr int UNITS = A4_UNITS;  // units per block (a block lies in one page)
   static constexpr int BK = UNITS * kKv4Unit;    // keys per block
   static constexpr int UB = kv4_unit_bytes(D, NG);
   static constexpr int STAGE = UNITS * UB;
-  static constexpr int STAGES = D == 256 ? 2 : 3;
+  static constexpr int STAGES = A4_STAGES;
   static constexpr int ROWS = 8 * NT;
   static constexpr int OP = D + 4;  // pitch of a row of the merge buffers (floats)
   static constexpr int RING = kWarps * STAGES * STAGE;
-  static constexpr int SMEM = RING + 2 * ROWS * OP * 4 + kWarps * ROWS * 8 + kWarps * STAGES * 8 + 64;
-  static constexpr int CTAS = SMEM <= 74 * 1024 ? 3 : (SMEM <= 112 * 1024 ? 2 : 1);  // per SM
+  static constexpr int SMEM = RING + ROWS * OP * 4 + kWarps * ROWS * 8 + kWarps * STAGES * 8 + 64;
+  static constexpr int CTAS = A4_CTAS;  // per SM
+  static constexpr bool ONES = NG <= 2;
 };
 
 template <bool BF16>
@@ -186,12 +196,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
   constexpr int J = kv4_j(D), NC = D / 32 / J, NW = D / 32, GW = NW / NG;
   constexpr int BK = C::BK, ROWS = C::ROWS;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* ring = smem + (threadIdx.x >> 5) * C::STAGES * C::STAGE;
-  float* obuf = reinterpret_cast<float*>(smem + C::RING);                    // [2][ROWS][OP]
-  float2* ml = reinterpret_cast<float2*>(obuf + 2 * ROWS * C::OP);           // [kWarps][ROWS]
+  uint8_t* ring = smem + static_cast<int>(threadIdx.x >> 5) * C::STAGES * C::STAGE;
+  float* obuf = reinterpret_cast<float*>(smem + C::RING);                    // [ROWS][OP]
+  float2* ml = reinterpret_cast<float2*>(obuf + ROWS * C::OP);           // [kWarps][ROWS]
   uint64_t* full = reinterpret_cast<uint64_t*>(ml + kWarps * ROWS) + (threadIdx.x >> 5) * C::STAGES;
   int64_t* sh = reinterpret_cast<int64_t*>(reinterpret_cast<uint64_t*>(ml + kWarps * ROWS) + kWarps * C::STAGES);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), g = lane >> 2, t = lane & 3;
 
   if (lane == 0) {
     for (int s = 0; s < C::STAGES; ++s) mbar_init(&full[s], 1);
@@ -256,34 +266,48 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
 
   // ---- the warp's stream of blocks: `pw` runs ahead of the consumer
   Walk<BK, ROWS> pw = cw;
-  int pu = pw.u0 + warp;
-  bool more = true;
-  const uint8_t* src = nullptr;  // the next block to copy (null: none)
-  auto seek = [&]() {
+  int pu = pw.u0 + warp, prow = 0;  // the next block, and its row in its page
+  const int* ptable = nullptr;      // ... whose table entry this is
+  const uint8_t* src = nullptr;     // the next block to copy (null: none)
+  auto place = [&]() {
+    const int key = (pw.it.blo + pu) * BK, page = key / p.page_size;
+    prow = key - page * p.page_size;
+    ptable = p.block_table + pw.it.seq * p.bt_stride + page;
+  };
+  auto seek = [&](bool fresh) {
+    bool more = true;
     while (more && (pu >= pw.ue || pw.it.hi <= pw.it.lo)) {
       more = pw.next(p);
       pu = pw.u0 + warp;
+      fresh = true;
     }
     src = nullptr;
     if (more) {
-      const int key = (pw.it.blo + pu) * BK, in_table = key / p.page_size, row = key - in_table * p.page_size;
-      int page = p.block_table[pw.it.seq * p.bt_stride + in_table];
+      if (fresh) place();
+      int page = *ptable;
       if (page < 0 || page >= p.num_pages) {
         record_error(p.status, kErrDeviceArg);
         page = 0;
       }
-      src = p.cache + page * p.c_st[0] + pw.it.kvh * p.c_st[1] + static_cast<int64_t>(row / kKv4Unit) * C::UB;
+      src = p.cache + page * p.c_st[0] + pw.it.kvh * p.c_st[1] + (prow / kKv4Unit) * C::UB;
       pu += kWarps;
+      prow += kWarps * BK;
+      while (prow >= p.page_size) {
+        prow -= p.page_size;
+        ++ptable;
+      }
     }
   };
   auto issue = [&](int slot) {
-    if (src != nullptr && lane == 0) {
-      mbar_arrive_expect_tx(&full[slot], C::STAGE);
-      bulk_load(ring + slot * C::STAGE, src, C::STAGE, &full[slot]);
+    if (src != nullptr) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&full[slot], C::STAGE);
+        bulk_load(ring + slot * C::STAGE, src, C::STAGE, &full[slot]);
+      }
+      seek(false);
     }
-    seek();
   };
-  seek();
+  seek(true);
 #pragma unroll
   for (int s = 0; s < C::STAGES; ++s) issue(s);
   int slot = 0;
@@ -295,8 +319,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
     const int R = p.sq * p.g;
     // ---- Q of the tile's rows as B operands; its row scales and group sums
     uint32_t qf[NW][2][NT][2];
-    float qs[NG][NT][2], rs[NT][2], m[NT][2], l[NT][2], tv[NG][NT][2], o[NW][2][NT][4];
+    float qs[NG][NT][2], rs[NT][2], m[NT][2], l[NT][2], tv[NG][NT][2], o[NW][2][NT][4], ones[C::ONES ? NG : 1][NT][4];
+    float cap_rs[NT][2];
     int row_hi[NT][2], row_lo[NT][2];
+    const bool capped = p.sc_b > 0.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = it.tile * ROWS + nt * 8 + g;
@@ -341,7 +367,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int from = 4 * (2 * t + c);
-        rs[nt][c] = __shfl_sync(0xffffffffu, down, from) * 0x1p24f * p.scale_log2;
+        const float scale = __shfl_sync(0xffffffffu, down, from) * 0x1p24f * p.scale_log2;
+        cap_rs[nt][c] = scale;
+        rs[nt][c] = capped ? 1.f : scale;
         const int rc = it.tile * ROWS + nt * 8 + 2 * t + c, pos = it.len - p.sq + rc / p.g;
         row_hi[nt][c] = rc < R ? pos : -1;
         row_lo[nt][c] = p.window_left >= 0 ? pos - p.window_left : 0;
@@ -357,6 +385,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
         for (int c = 0; c < 2; ++c) {
           qs[q][nt][c] = __shfl_sync(0xffffffffu, sum[q], 4 * (2 * t + c));
           tv[q][nt][c] = 0.f;
+        }
+        if (C::ONES) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ones[q][nt][e] = 0.f;
         }
       }
 #pragma unroll
@@ -424,19 +456,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
             }
           }
         }
-#pragma unroll
-        for (int mt = 0; mt < 2 * C::UNITS; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[mt][nt][e] *= rs[nt][e & 1];
-        if (p.sc_b > 0.f) {
+        if (capped) {  // (from here on the scores are final: rs is 1)
 #pragma unroll
           for (int mt = 0; mt < 2 * C::UNITS; ++mt)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s[mt][nt][e] = p.sc_b * tanh_from_exp2_arg(p.sc_k * s[mt][nt][e]);
+              for (int e = 0; e < 4; ++e)
+                s[mt][nt][e] = p.sc_b * tanh_from_exp2_arg(p.sc_k * (s[mt][nt][e] * cap_rs[nt][e & 1]));
         }
         if (edge) {
 #pragma unroll
@@ -451,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
         }
         // ---- running maximum; O, l and the rest follow it when it grows
         bool grown = false;
-        float mn[NT][2];
+        float mn[NT][2], ref[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -462,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            mn[nt][c] = fmaxf(m[nt][c], x);
+            mn[nt][c] = fmaxf(m[nt][c], x * rs[nt][c]);
             grown = grown || mn[nt][c] > m[nt][c];
           }
         if (__any_sync(0xffffffffu, grown)) {
@@ -474,7 +501,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
               m[nt][c] = mn[nt][c];
               l[nt][c] *= a;
 #pragma unroll
-              for (int q = 0; q < NG; ++q) tv[q][nt][c] *= a;
+              for (int q = 0; q < NG; ++q) {
+                tv[q][nt][c] *= a;
+                if (C::ONES) ones[q][nt][c] *= a;
+              }
 #pragma unroll
               for (int j = 0; j < NW; ++j) {
                 o[j][0][nt][c] *= a;
@@ -484,6 +514,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
               }
             }
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) ref[nt][c] = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
         // ---- V's weights stay in fp16's normal range: times a power of two that puts the
         // first block's largest scale at 2^7..2^8 and is lowered when one passes 2^15
         {
@@ -503,6 +537,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
             const float now = __uint_as_float((261u - (__float_as_uint(top) >> 23)) << 23);
             if (vscale > 0.f) {
               const float a = now / vscale;
+              if (C::ONES) {
+#pragma unroll
+                for (int q = 0; q < NG; ++q)
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) {
+                    ones[q][nt][0] *= a;
+                    ones[q][nt][1] *= a;
+                  }
+              }
 #pragma unroll
               for (int j = 0; j < NW; ++j)
 #pragma unroll
@@ -538,8 +581,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float ref = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
-              pr[nt][e] = ex2_approx(s[mt][nt][e] - ref);
+              pr[nt][e] = ex2_approx(fmaf(s[mt][nt][e], rs[nt][e & 1], -ref[nt][e & 1]));
               l[nt][e & 1] += pr[nt][e];
             }
           uint32_t bw[NG][NT][2];
@@ -552,12 +594,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
             for (int nt = 0; nt < NT; ++nt) {
               const uint32_t ha = pack_f16(pr[nt][0] * va, pr[nt][1] * va);
               const uint32_t hb = pack_f16(pr[nt][2] * vb, pr[nt][3] * vb);
-              const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&ha));
-              const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&hb));
-              tv[q][nt][0] = fmaf(pr[nt][0], na, fmaf(pr[nt][2], nb, fmaf(fa.x + fb.x, off8, tv[q][nt][0])));
-              tv[q][nt][1] = fmaf(pr[nt][1], na, fmaf(pr[nt][3], nb, fmaf(fa.y + fb.y, off8, tv[q][nt][1])));
+              tv[q][nt][0] = fmaf(pr[nt][0], na, fmaf(pr[nt][2], nb, tv[q][nt][0]));
+              tv[q][nt][1] = fmaf(pr[nt][1], na, fmaf(pr[nt][3], nb, tv[q][nt][1]));
+              if (!C::ONES) {
+                const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&ha));
+                const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&hb));
+                tv[q][nt][0] = fmaf(fa.x + fb.x, off8, tv[q][nt][0]);
+                tv[q][nt][1] = fmaf(fa.y + fb.y, off8, tv[q][nt][1]);
+              }
               bw[q][nt][0] = transpose8(ha);
               bw[q][nt][1] = transpose8(hb);
+              if (C::ONES)  // the sum of the weights as rounded, in units of 2^-24
+                mma16816(ones[q][nt], 0x00010001u, 0u, 0x00010001u, 0u, bw[q][nt][0], bw[q][nt][1]);
             }
           }
           const uint8_t* vu = unit + 16 * D;
@@ -588,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
         }
       }
 
-    // ---- the warps' shares of the segment: common maximum, then O through two buffers
+    // ---- the warps' shares of the segment: common maximum, then O warp by warp into one buffer
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -607,10 +655,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
     }
     __syncthreads();
     const float unscale = vscale > 0.f ? 0x1p24f / vscale : 0.f;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (warp / 2 == half) {
-        float* ob = obuf + (warp & 1) * ROWS * C::OP;
+#pragma unroll 1
+    for (int turn = 0; turn < kWarps; ++turn) {
+      if (warp == turn) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -622,11 +669,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
             const float a = m[nt][c] == -INFINITY ? 0.f : ex2_approx(m[nt][c] - M), au = a * unscale;
 #pragma unroll
             for (int j = 0; j < NW; ++j) {
-              const float add = a * tv[j / GW][nt][c];
+              float add = a * tv[j / GW][nt][c];
+              if (C::ONES) add = fmaf(ones[j / GW][nt][c], -8.f * au, add);
               float4 x = make_float4(fmaf(o[j][0][nt][c], au, add), fmaf(o[j][0][nt][c + 2], au * 0.0625f, add),
                                      fmaf(o[j][1][nt][c], au, add), fmaf(o[j][1][nt][c + 2], au * 0.0625f, add));
-              float4* dst = reinterpret_cast<float4*>(ob + r * C::OP + 32 * j + 4 * g);
-              if (half == 1) {
+              float4* dst = reinterpret_cast<float4*>(obuf + r * C::OP + 32 * j + 4 * g);
+              if (turn > 0) {
                 const float4 y = *dst;
                 x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
               }
@@ -647,10 +695,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
     if (!whole) {
       for (int x = threadIdx.x; x < ROWS * PER; x += kThreads) {
         const int r = x / PER, e = x % PER;
-        const float4 a = *reinterpret_cast<const float4*>(obuf + r * C::OP + 4 * e);
-        const float4 b = *reinterpret_cast<const float4*>(obuf + (ROWS + r) * C::OP + 4 * e);
         reinterpret_cast<float4*>(p.part_o)[(static_cast<int64_t>(my) * ROWS + r) * PER + e] =
-            make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+            *reinterpret_cast<const float4*>(obuf + r * C::OP + 4 * e);
       }
       if (threadIdx.x < ROWS) {
         float M = -INFINITY, L = 0.f;
@@ -684,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
             if (y.x != -INFINITY) L = fmaf(y.y, ex2_approx(y.x - M), L);
           }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = obuf[r * C::OP + 8 * e + k] + obuf[(ROWS + r) * C::OP + 8 * e + k];
+          for (int k = 0; k < 8; ++k) f[k] = obuf[r * C::OP + 8 * e + k];
         } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k) f[k] = 0.f;
