@@ -36,35 +36,37 @@
 namespace fa {
 namespace attend4 {
 
-constexpr int kWarps = 4;
+#ifndef A4_WARPS
+#define A4_WARPS 4
+#endif
+#ifndef A4_GAP
+#define A4_GAP 12
+#endif
+constexpr int kWarps = A4_WARPS;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMinBlocks = kWarps;  // blocks a CTA takes at least: one for each warp
+constexpr int kGap = A4_GAP;        // what an item costs besides its blocks, in blocks
+constexpr int kMinShare = 8 + kGap;  // a CTA's stretch of the line at least ...
+constexpr int kUncut = 16;      // ... and items of up to so many blocks are never cut
+constexpr int kMostParts = 64;  // CTAs that share an item at most
 constexpr float kLn2 = 0.69314718055994530942f;
 
 enum : int { kSiteFull = 48 };
 
 template <int D, int NG, int NT>
 struct Cfg {
-#ifndef A4_UNITS
-#define A4_UNITS (D == 64 ? 2 : 1)
-#endif
-#ifndef A4_STAGES
-#define A4_STAGES (D == 256 ? 2 : 3)
-#endif
-#ifndef A4_CTAS
-#define A4_CTAS (SMEM <= 74 * 1024 ? 3 : (SMEM <= 112 * 1024 ? 2 : 1))
-#endif
-  static constexpr int UNITS = A4_UNITS;  // units per block (a block lies in one page)
-  static constexpr int BK = UNITS * kKv4Unit;    // keys per block
+  static constexpr int UNITS = D == 256 || (kWarps == 8 && NT == 2) ? 1 : 2;  // units per block (a block lies in one page)
+  static constexpr int BK = UNITS * kKv4Unit;     // keys per block
   static constexpr int UB = kv4_unit_bytes(D, NG);
   static constexpr int STAGE = UNITS * UB;
-  static constexpr int STAGES = A4_STAGES;
+  static constexpr int STAGES = 2;
   static constexpr int ROWS = 8 * NT;
-  static constexpr int OP = D + 4;  // pitch of a row of the merge buffers (floats)
+  static constexpr int DP = D < 128 ? D : 128;  // dims of O that the warps exchange at a time
+  static constexpr int OP = DP + 4;             // pitch of a row there (floats)
   static constexpr int RING = kWarps * STAGES * STAGE;
-  static constexpr int SMEM = RING + ROWS * OP * 4 + kWarps * ROWS * 8 + kWarps * STAGES * 8 + 64;
-  static constexpr int CTAS = A4_CTAS;  // per SM
-  static constexpr bool ONES = NG <= 2;
+  static constexpr int SMEM = RING + kWarps * ROWS * OP * 4 + kWarps * ROWS * 8 + kWarps * STAGES * 8 + 16;
+  static constexpr int CTAS = kWarps == 8 ? 1 : NT == 1 && SMEM <= 74 * 1024 ? 3 : (SMEM <= 112 * 1024 ? 2 : 1);  // per SM
+  static constexpr bool ONES = NG <= 2 || (NG == 4 && NT == 1);
+  static_assert(kMostParts * ROWS * 4 <= kWarps * ROWS * OP * 4, "the merge's weights fit the exchange buffer");
 };
 
 template <bool BF16>
@@ -130,21 +132,19 @@ __device__ __forceinline__ int seq_len(const Attend4Params& p, int seq) {
   return n > 0 ? n : 0;
 }
 
-// Keys [lo, hi) that the rows of a tile see, all in all.
-__device__ __forceinline__ void tile_range(const Attend4Params& p, int len, int rows, int tile, int* lo, int* hi) {
-  const int r1 = min(p.sq * p.g, (tile + 1) * rows) - 1;
-  const int first = len - p.sq + tile * rows / p.g, last = len - p.sq + r1 / p.g;
-  *hi = max(last + 1, 0);
-  *lo = p.window_left >= 0 ? max(0, first - p.window_left) : 0;
-}
-
-// One item: a row tile of one KV head of one sequence, n blocks from blo on (one,
-// with nothing in it, where no row sees a key).
+// One item: a row tile of one KV head of one sequence, keys [lo, hi) all in all, n
+// blocks from blo on (one, with nothing in it, where no row sees a key).
 template <int BK, int ROWS>
 struct Item {
   int seq, kvh, tile, len, lo, hi, blo, n;
   __device__ __forceinline__ void range(const Attend4Params& p) {
-    tile_range(p, len, ROWS, tile, &lo, &hi);
+    int first = len - p.sq, last = first;  // positions of the tile's first and last row
+    if (p.sq > 1) {
+      first += tile * ROWS / p.g;
+      last += (min(p.sq * p.g, (tile + 1) * ROWS) - 1) / p.g;
+    }
+    hi = max(last + 1, 0);
+    lo = p.window_left >= 0 ? max(0, first - p.window_left) : 0;
     blo = lo / BK;
     n = hi > lo ? (hi + BK - 1) / BK - blo : 1;
   }
@@ -160,15 +160,18 @@ struct Item {
   }
 };
 
-// A CTA's stretch of the line, item by item: blocks [u0, ue) of the current one.
+// A CTA's stretch of the line, item by item: blocks [u0, ue) of the current one.  On
+// the line every item's blocks follow a gap of kGap positions, so that a CTA that ends
+// one item and begins the next gets less of both.  An item of few blocks belongs to
+// the CTA in whose stretch its first block lies.
 template <int BK, int ROWS>
 struct Walk {
   Item<BK, ROWS> it;
   int u0, ue;
-  int left;  // blocks of the CTA from u0 on
-  __device__ __forceinline__ void enter() { ue = min(it.n, u0 + left); }
+  int left;  // blocks from u0 to the end of the stretch
+  __device__ __forceinline__ void enter() { ue = it.n <= kUncut ? it.n : min(it.n, u0 + left); }
   __device__ __forceinline__ bool next(const Attend4Params& p) {  // false: nothing is left
-    left -= ue - u0;
+    left -= ue - u0 + kGap;
     if (left <= 0) return false;
     it.next(p);
     u0 = 0;
@@ -177,17 +180,52 @@ struct Walk {
   }
 };
 
-// Blocks of one sequence (all its KV heads and tiles).
+// Line positions of one KV head of a sequence, all tiles; `most`: blocks of its largest item.
 template <int BK, int ROWS>
-__device__ __forceinline__ int64_t seq_blocks(const Attend4Params& p, int seq) {
+__device__ __forceinline__ int head_blocks(const Attend4Params& p, int seq, int* most) {
   Item<BK, ROWS> it;
   it.len = seq_len(p, seq);
-  int64_t n = 0;
-  for (it.tile = 0; it.tile < p.ntiles; ++it.tile) {
+  it.tile = p.ntiles - 1;
+  it.range(p);
+  int n = it.n + kGap;
+  *most = it.n;
+  if (p.sq == 1) return n * p.ntiles;  // every tile sees the same keys
+  for (it.tile = 0; it.tile < p.ntiles - 1; ++it.tile) {
     it.range(p);
-    n += it.n;
+    n += it.n + kGap;
+    *most = max(*most, it.n);
   }
-  return n * p.hkv;
+  return n;
+}
+
+// Eight dims of a finished row, times inv, and its LSE (M, L: log2 maximum and sum).
+template <int D, bool BF16>
+__device__ __forceinline__ void store_row(const Attend4Params& p, int seq, int kvh, int row, int dim, const float* f,
+                                          float inv) {
+  const int qi = p.sq > 1 ? row / p.g : 0, h = kvh * p.g + row - qi * p.g;
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (BF16) {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(f[2 * k] * inv, f[2 * k + 1] * inv);
+      w[k] = *reinterpret_cast<const uint32_t*>(&x);
+    } else {
+      w[k] = pack_f16(f[2 * k] * inv, f[2 * k + 1] * inv);
+    }
+  }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + seq * p.o_st[0] + qi * p.o_st[1] + h * p.o_st[2] + dim) =
+      make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void store_lse(const Attend4Params& p, int seq, int kvh, int row, float M, float L) {
+  const int qi = p.sq > 1 ? row / p.g : 0, h = kvh * p.g + row - qi * p.g;
+  p.lse[(static_cast<int64_t>(seq) * p.hq + h) * p.sq + qi] = L > 0.f ? (M + lg2_approx(L)) * kLn2 : -INFINITY;
+}
+
+__device__ __forceinline__ int count_in(int* counter) {
+  int old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+  return old;
 }
 
 template <int D, int NG, bool BF16, int NT>
@@ -196,100 +234,127 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
   constexpr int J = kv4_j(D), NC = D / 32 / J, NW = D / 32, GW = NW / NG;
   constexpr int BK = C::BK, ROWS = C::ROWS;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* ring = smem + static_cast<int>(threadIdx.x >> 5) * C::STAGES * C::STAGE;
-  float* obuf = reinterpret_cast<float*>(smem + C::RING);                    // [ROWS][OP]
-  float2* ml = reinterpret_cast<float2*>(obuf + ROWS * C::OP);           // [kWarps][ROWS]
-  uint64_t* full = reinterpret_cast<uint64_t*>(ml + kWarps * ROWS) + (threadIdx.x >> 5) * C::STAGES;
-  int64_t* sh = reinterpret_cast<int64_t*>(reinterpret_cast<uint64_t*>(ml + kWarps * ROWS) + kWarps * C::STAGES);
   const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), g = lane >> 2, t = lane & 3;
+  uint8_t* ring = smem + warp * C::STAGES * C::STAGE;
+  float* obuf = reinterpret_cast<float*>(smem + C::RING);               // [kWarps][ROWS][OP]
+  float2* ml = reinterpret_cast<float2*>(obuf + kWarps * ROWS * C::OP);  // [kWarps][ROWS]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ml + kWarps * ROWS);
+  uint64_t* full = bars + warp * C::STAGES;
+  int* last_in = reinterpret_cast<int*>(bars + kWarps * C::STAGES);
 
   if (lane == 0) {
     for (int s = 0; s < C::STAGES; ++s) mbar_init(&full[s], 1);
     fence_mbar_init();
   }
-  // ---- the CTA's stretch of the line of blocks: total, then the sequence where it starts
-  int64_t total = 0;
-  for (int s = threadIdx.x; s < p.b; s += kThreads) total += seq_blocks<BK, ROWS>(p, s);
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
-  if (lane == 0) sh[warp] = total;
-  __syncthreads();
-  total = sh[0] + sh[1] + sh[2] + sh[3];
-  int64_t share64 = (total + gridDim.x - 1) / gridDim.x;
-  if (share64 < kMinBlocks) share64 = kMinBlocks;
-  const int share = static_cast<int>(share64);
-  const int64_t begin = static_cast<int64_t>(blockIdx.x) * share;
-  if (begin >= total) return;
-  __syncthreads();
-  if (warp == 0) {
-    int64_t before = 0;
+  __syncwarp();
+  // ---- the CTA's stretch of the line of blocks, found by every warp for itself: the
+  // total, the share of a CTA, the sequence where this one's stretch begins
+  Walk<BK, ROWS> cw;
+  int share, item_at;  // where the current item's blocks start on the line
+  {
+    int mine = 0, head = 0, most = 0;
+    for (int s = lane; s < p.b; s += 32) {
+      int m1;
+      head = head_blocks<BK, ROWS>(p, s, &m1);
+      mine += head * p.hkv;
+      most = max(most, m1);
+    }
+    const int total = __reduce_add_sync(0xffffffffu, mine);
+    most = __reduce_max_sync(0xffffffffu, most);
+    share = static_cast<int>((static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x);
+    share = max(max(share, kMinShare), (most + kMostParts - 2) / (kMostParts - 1));
+    if (blockIdx.x > static_cast<unsigned>(total - 1) / static_cast<unsigned>(share)) return;
+    const int begin = static_cast<int>(blockIdx.x) * share;
+    int before = 0, rem = 0;
     for (int s0 = 0; s0 < p.b; s0 += 32) {
-      const int64_t n = s0 + lane < p.b ? seq_blocks<BK, ROWS>(p, s0 + lane) : 0;
-      int64_t incl = n;
+      if (p.b > 32) {
+        int m1;
+        head = s0 + lane < p.b ? head_blocks<BK, ROWS>(p, s0 + lane, &m1) : 0;
+        mine = head * p.hkv;
+      }
+      int incl = mine;
 #pragma unroll
       for (int x = 1; x < 32; x <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, x);
+        const int y = __shfl_up_sync(0xffffffffu, incl, x);
         if (lane >= x) incl += y;
       }
       const unsigned hit = __ballot_sync(0xffffffffu, begin < before + incl);
       if (hit != 0) {
-        if (lane == __ffs(hit) - 1) {
-          sh[4] = s0 + lane;
-          sh[5] = begin - (before + incl - n);
-        }
+        const int at = __ffs(hit) - 1;
+        cw.it.seq = s0 + at;
+        rem = begin - before - __shfl_sync(0xffffffffu, incl - mine, at);
+        head = __shfl_sync(0xffffffffu, head, at);
         break;
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
-  }
-  __syncthreads();
-  Walk<BK, ROWS> cw;
-  cw.left = static_cast<int>(min(total - begin, static_cast<int64_t>(share)));
-  cw.it.seq = static_cast<int>(sh[4]);
-  cw.it.len = seq_len(p, cw.it.seq);
-  {
-    int64_t rem = sh[5];
-    const int64_t per_head = seq_blocks<BK, ROWS>(p, cw.it.seq) / p.hkv;
-    cw.it.kvh = static_cast<int>(rem / per_head);
-    rem %= per_head;
+    cw.left = min(total - begin, share);
+    cw.it.len = seq_len(p, cw.it.seq);
+    cw.it.kvh = rem / head;
+    int u = rem - cw.it.kvh * head - kGap;  // (negative: in the gap)
     cw.it.tile = 0;
     cw.it.range(p);
-    while (rem >= cw.it.n) {
-      rem -= cw.it.n;
+    while (u >= cw.it.n) {
+      u -= cw.it.n + kGap;
       ++cw.it.tile;
       cw.it.range(p);
     }
-    cw.u0 = static_cast<int>(rem);
+    item_at = begin - u;
+    if (u < 0) {
+      cw.left += u;
+      if (cw.left <= 0) return;
+    }
+    cw.u0 = max(u, 0);
     cw.enter();
+    if (u > 0 && cw.it.n <= kUncut) {  // an earlier CTA has this one whole
+      item_at += cw.it.n + kGap;
+      if (!cw.next(p)) return;
+    }
   }
-  const int64_t item0 = begin - cw.u0;  // where the first item starts on the line
+  const int R = p.sq * p.g;
 
-  // ---- the warp's stream of blocks: `pw` runs ahead of the consumer
+  // ---- Q of a tile's rows, as stored (row 8 nt + g, dims 32 j + 8 t ..): loaded ahead
+  uint4 qraw[NT][NW];
+  auto load_q = [&]() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = cw.it.tile * ROWS + nt * 8 + g;
+      const int qi = p.sq > 1 ? r / p.g : 0, h = r - qi * p.g;
+      const uint16_t* at = static_cast<const uint16_t*>(p.q) + cw.it.seq * p.q_st[0] + qi * p.q_st[1] +
+                           (cw.it.kvh * p.g + h) * p.q_st[2] + 8 * t;
+#pragma unroll
+      for (int j = 0; j < NW; ++j)
+        qraw[nt][j] = r < R ? *reinterpret_cast<const uint4*>(at + 32 * j) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  load_q();
+
+  // ---- the warp's stream of blocks: `pw` runs ahead of the consumer, and the page of
+  // the block after the copies in flight is on its way from the block table
   Walk<BK, ROWS> pw = cw;
-  int pu = pw.u0 + warp, prow = 0;  // the next block, and its row in its page
-  const int* ptable = nullptr;      // ... whose table entry this is
-  const uint8_t* src = nullptr;     // the next block to copy (null: none)
+  int pu = pw.u0 + warp, prow = 0;  // the block after the next, and its row in its page
+  const int* ptable = nullptr;      // ... and its table entry
+  struct Next {
+    int page;  // -1: no block is left
+    int64_t off;
+  };
   auto place = [&]() {
     const int key = (pw.it.blo + pu) * BK, page = key / p.page_size;
     prow = key - page * p.page_size;
     ptable = p.block_table + pw.it.seq * p.bt_stride + page;
   };
+  bool more = true;
   auto seek = [&](bool fresh) {
-    bool more = true;
     while (more && (pu >= pw.ue || pw.it.hi <= pw.it.lo)) {
       more = pw.next(p);
       pu = pw.u0 + warp;
       fresh = true;
     }
-    src = nullptr;
+    Next n{0, -1};
     if (more) {
       if (fresh) place();
-      int page = *ptable;
-      if (page < 0 || page >= p.num_pages) {
-        record_error(p.status, kErrDeviceArg);
-        page = 0;
-      }
-      src = p.cache + page * p.c_st[0] + pw.it.kvh * p.c_st[1] + (prow / kKv4Unit) * C::UB;
+      n.page = *ptable;
+      n.off = pw.it.kvh * p.c_st[1] + (prow / kKv4Unit) * C::UB;
       pu += kWarps;
       prow += kWarps * BK;
       while (prow >= p.page_size) {
@@ -297,26 +362,34 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
         ++ptable;
       }
     }
+    return n;
   };
-  auto issue = [&](int slot) {
-    if (src != nullptr) {
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&full[slot], C::STAGE);
-        bulk_load(ring + slot * C::STAGE, src, C::STAGE, &full[slot]);
-      }
-      seek(false);
+  auto copy = [&](const Next& n, int slot) {
+    int page = n.page;
+    if (page < 0 || page >= p.num_pages) {
+      record_error(p.status, kErrDeviceArg);
+      page = 0;
+    }
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&full[slot], C::STAGE);
+      bulk_load(ring + slot * C::STAGE, p.cache + page * p.c_st[0] + n.off, C::STAGE, &full[slot]);
     }
   };
-  seek(true);
+  Next next;
+  {
+    Next first[C::STAGES];
 #pragma unroll
-  for (int s = 0; s < C::STAGES; ++s) issue(s);
+    for (int s = 0; s < C::STAGES; ++s) first[s] = seek(s == 0);
+    next = seek(false);
+#pragma unroll
+    for (int s = 0; s < C::STAGES; ++s)
+      if (first[s].off >= 0) copy(first[s], s);
+  }
   int slot = 0;
   uint32_t phase = 0;
 
-  int64_t item_at = item0;
   for (bool live = true; live;) {
-    const auto& it = cw.it;
-    const int R = p.sq * p.g;
+    const Item<BK, ROWS> it = cw.it;
     // ---- Q of the tile's rows as B operands; its row scales and group sums
     uint32_t qf[NW][2][NT][2];
     float qs[NG][NT][2], rs[NT][2], m[NT][2], l[NT][2], tv[NG][NT][2], o[NW][2][NT][4], ones[C::ONES ? NG : 1][NT][4];
@@ -325,16 +398,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
     const bool capped = p.sc_b > 0.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = it.tile * ROWS + nt * 8 + g;
-      uint4 u[NW];
-#pragma unroll
-      for (int j = 0; j < NW; ++j) {
-        u[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < R)
-          u[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + it.seq * p.q_st[0] +
-                                                 (r / p.g) * p.q_st[1] + (it.kvh * p.g + r % p.g) * p.q_st[2] +
-                                                 32 * j + 8 * t);
-      }
+      const uint4(&u)[NW] = qraw[nt];
       // the row is scaled by a power of two so that its largest value lies in [2^14, 2^15)
       float top = 0.f;
 #pragma unroll
@@ -370,7 +434,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
         const float scale = __shfl_sync(0xffffffffu, down, from) * 0x1p24f * p.scale_log2;
         cap_rs[nt][c] = scale;
         rs[nt][c] = capped ? 1.f : scale;
-        const int rc = it.tile * ROWS + nt * 8 + 2 * t + c, pos = it.len - p.sq + rc / p.g;
+        const int rc = it.tile * ROWS + nt * 8 + 2 * t + c;
+        const int pos = it.len - p.sq + (p.sq > 1 ? rc / p.g : 0);
         row_hi[nt][c] = rc < R ? pos : -1;
         row_lo[nt][c] = p.window_left >= 0 ? pos - p.window_left : 0;
         m[nt][c] = -INFINITY;
@@ -397,9 +462,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
         for (int e = 0; e < 4; ++e) o[j][0][nt][e] = o[j][1][nt][e] = 0.f;
     }
     // keys that every row of the tile sees: no mask there
-    const int all_hi = it.len - p.sq + it.tile * ROWS / p.g;
-    const int all_lo = p.window_left >= 0
-                           ? max(0, it.len - p.sq + (min(R, (it.tile + 1) * ROWS) - 1) / p.g - p.window_left) : 0;
+    int all_hi = it.len - p.sq, all_lo = it.hi - 1 - p.window_left;
+    if (p.sq > 1) all_hi += it.tile * ROWS / p.g;
+    if (p.window_left < 0) all_lo = 0;
     float vscale = 0.f;  // V's weights are held times this power of two (0: not chosen yet)
 
     if (it.hi > it.lo)
@@ -629,14 +694,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
           }
         }
         __syncwarp();  // every lane has read the stage
-        issue(slot);
+        if (next.off >= 0) {
+          copy(next, slot);
+          next = seek(false);
+        }
         if (++slot == C::STAGES) {
           slot = 0;
           phase ^= 1u;
         }
       }
 
-    // ---- the warps' shares of the segment: common maximum, then O warp by warp into one buffer
+    // ---- the next item is found and its Q loaded while this one's shares are joined
+    const int at = item_at;
+    item_at += it.n + kGap;
+    live = cw.next(p);
+    if (live) load_q();
+
+    // ---- the warps' shares: each row's maximum, sum and O (as of the warp's maximum)
+    // through shared memory, dims [128 ps, 128 ps + DP) at a time
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -653,130 +728,128 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
 #pragma unroll
         for (int c = 0; c < 2; ++c) ml[warp * ROWS + nt * 8 + 2 * t + c] = make_float2(m[nt][c], l[nt][c]);
     }
-    __syncthreads();
     const float unscale = vscale > 0.f ? 0x1p24f / vscale : 0.f;
-#pragma unroll 1
-    for (int turn = 0; turn < kWarps; ++turn) {
-      if (warp == turn) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int r = nt * 8 + 2 * t + c;
-            float M = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * ROWS + r].x);
-            const float a = m[nt][c] == -INFINITY ? 0.f : ex2_approx(m[nt][c] - M), au = a * unscale;
-#pragma unroll
-            for (int j = 0; j < NW; ++j) {
-              float add = a * tv[j / GW][nt][c];
-              if (C::ONES) add = fmaf(ones[j / GW][nt][c], -8.f * au, add);
-              float4 x = make_float4(fmaf(o[j][0][nt][c], au, add), fmaf(o[j][0][nt][c + 2], au * 0.0625f, add),
-                                     fmaf(o[j][1][nt][c], au, add), fmaf(o[j][1][nt][c + 2], au * 0.0625f, add));
-              float4* dst = reinterpret_cast<float4*>(obuf + r * C::OP + 32 * j + 4 * g);
-              if (turn > 0) {
-                const float4 y = *dst;
-                x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-              }
-              *dst = x;
-            }
-          }
-      }
-      __syncthreads();
+    const int cta = blockIdx.x;
+    int c0 = cta, c1 = cta;  // the CTAs that hold the item
+    if (it.n > kUncut) {
+      c0 = at / share;
+      c1 = (at + it.n - 1) / share;
     }
-
-    // ---- out: the whole item, or a partial of it
-    const int64_t c0 = item_at / share, c1 = (item_at + it.n - 1) / share;  // the CTAs that hold the item
     const bool whole = c0 == c1;
-    const int64_t cta = blockIdx.x;
-    const int my = static_cast<int>(2 * cta + (cta == c0 && item_at > c0 * share ? 1 : 0));
-    constexpr int PER = D / 4;  // float4 of a row
-    bool merge = false;
-    if (!whole) {
-      for (int x = threadIdx.x; x < ROWS * PER; x += kThreads) {
-        const int r = x / PER, e = x % PER;
-        reinterpret_cast<float4*>(p.part_o)[(static_cast<int64_t>(my) * ROWS + r) * PER + e] =
-            *reinterpret_cast<const float4*>(obuf + r * C::OP + 4 * e);
-      }
-      if (threadIdx.x < ROWS) {
-        float M = -INFINITY, L = 0.f;
+    const int s0 = 2 * c0 + (at > c0 * share ? 1 : 0);  // the first part's slot
+    const int my = cta == c0 ? s0 : 2 * cta;
+    constexpr int PER = C::DP / 8;  // threads of a row
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * ROWS + threadIdx.x].x);
+    for (int ps = 0; ps < D / C::DP; ++ps) {
+      if (ps > 0) __syncthreads();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int j = 0; j < C::DP / 32; ++j) {
+            const int w = ps * (C::DP / 32) + j;
+            float add = tv[w / GW][nt][c];
+            if (C::ONES) add = fmaf(ones[w / GW][nt][c], -8.f * unscale, add);
+            *reinterpret_cast<float4*>(obuf + (warp * ROWS + nt * 8 + 2 * t + c) * C::OP + 32 * j + 4 * g) =
+                make_float4(fmaf(o[w][0][nt][c], unscale, add), fmaf(o[w][0][nt][c + 2], unscale * 0.0625f, add),
+                            fmaf(o[w][1][nt][c], unscale, add), fmaf(o[w][1][nt][c + 2], unscale * 0.0625f, add));
+          }
+      __syncthreads();
+      for (int x = threadIdx.x; x < ROWS * PER; x += kThreads) {
+        const int r = x / PER, e = x % PER, row = it.tile * ROWS + r;
+        float M = -INFINITY, L = 0.f, f[8];
+        float2 y[kWarps];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float2 x = ml[w * ROWS + threadIdx.x];
-          if (x.x != -INFINITY) L = fmaf(x.y, ex2_approx(x.x - M), L);
+          y[w] = ml[w * ROWS + r];
+          M = fmaxf(M, y[w].x);
         }
-        p.part_ml[static_cast<int64_t>(my) * ROWS + threadIdx.x] = make_float2(M, L);
-      }
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) sh[0] = atomicAdd(p.counters + c0, 1) == static_cast<int>(c1 - c0);
-      __syncthreads();
-      merge = sh[0] != 0;
-      if (merge) __threadfence();
-    }
-    if (whole || merge) {
-      for (int x = threadIdx.x; x < ROWS * (D / 8); x += kThreads) {
-        const int r = x / (D / 8), e = x % (D / 8), row = it.tile * ROWS + r;
-        if (row >= R) continue;
-        float f[8], M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float a = y[w].x == -INFINITY ? 0.f : ex2_approx(y[w].x - M);
+          const float4* from = reinterpret_cast<const float4*>(obuf + (w * ROWS + r) * C::OP + 8 * e);
+          const float4 u = from[0], v = from[1];
+          L = fmaf(y[w].y, a, L);
+          f[0] = fmaf(u.x, a, f[0]);
+          f[1] = fmaf(u.y, a, f[1]);
+          f[2] = fmaf(u.z, a, f[2]);
+          f[3] = fmaf(u.w, a, f[3]);
+          f[4] = fmaf(v.x, a, f[4]);
+          f[5] = fmaf(v.y, a, f[5]);
+          f[6] = fmaf(v.z, a, f[6]);
+          f[7] = fmaf(v.w, a, f[7]);
+        }
         if (whole) {
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * ROWS + r].x);
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float2 y = ml[w * ROWS + r];
-            if (y.x != -INFINITY) L = fmaf(y.y, ex2_approx(y.x - M), L);
+          if (row < R) store_row<D, BF16>(p, it.seq, it.kvh, row, ps * C::DP + 8 * e, f, L > 0.f ? 1.f / L : 0.f);
+          if (row < R && e == 0 && ps == 0) store_lse(p, it.seq, it.kvh, row, M, L);
+        } else {
+          float4* to = reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(my) * ROWS + r) * D + ps * C::DP + 8 * e);
+          to[0] = make_float4(f[0], f[1], f[2], f[3]);
+          to[1] = make_float4(f[4], f[5], f[6], f[7]);
+          if (e == 0 && ps == 0) p.part_ml[static_cast<int64_t>(my) * ROWS + r] = make_float2(M, L);
+        }
+      }
+    }
+    if (!whole) {
+      // the last of the item's CTAs to get here joins the parts (the barrier puts the
+      // CTA's stores before thread 0's releasing and acquiring count)
+      __syncthreads();
+      if (threadIdx.x == 0) *last_in = count_in(p.counters + c0) == c1 - c0;
+      __syncthreads();
+      if (*last_in) {
+        constexpr int TPR = kThreads / ROWS;  // threads of a row for the weights
+        float* wbuf = obuf;                   // [parts][ROWS]
+        const int parts = c1 - c0 + 1;
+        {
+          const int r = threadIdx.x / TPR, k = threadIdx.x % TPR, row = it.tile * ROWS + r;
+          float M = -INFINITY, L = 0.f;
+          for (int s = k; s < parts; s += TPR) {
+            const float2 y = __ldcg(&p.part_ml[static_cast<int64_t>(s == 0 ? s0 : 2 * (c0 + s)) * ROWS + r]);
+            const float n = fmaxf(M, y.x);
+            if (n != -INFINITY) L = L * ex2_approx(M - n) + (y.x == -INFINITY ? 0.f : y.y * ex2_approx(y.x - n));
+            M = n;
+            wbuf[s * ROWS + r] = y.x;
           }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = obuf[r * C::OP + 8 * e + k];
-        } else {
+          for (int x = 1; x < TPR; x <<= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, M, x), l2 = __shfl_xor_sync(0xffffffffu, L, x);
+            const float n = fmaxf(M, m2);
+            if (n != -INFINITY) L = L * ex2_approx(M - n) + l2 * ex2_approx(m2 - n);
+            M = n;
+          }
+          const float inv = L > 0.f ? 1.f / L : 0.f;
+          for (int s = k; s < parts; s += TPR)
+            wbuf[s * ROWS + r] = M == -INFINITY ? 0.f : ex2_approx(wbuf[s * ROWS + r] - M) * inv;
+          if (k == 0 && row < R) store_lse(p, it.seq, it.kvh, row, M, L);
+        }
+        __syncthreads();
+        for (int x = threadIdx.x; x < ROWS * (D / 8); x += kThreads) {
+          const int r = x / (D / 8), e = x % (D / 8), row = it.tile * ROWS + r;
+          float f[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) f[k] = 0.f;
-          const int s0 = static_cast<int>(2 * c0 + (item_at > c0 * share ? 1 : 0));
-          for (int64_t c = c0; c <= c1; ++c)
-            M = fmaxf(M, __ldcg(&p.part_ml[(c == c0 ? s0 : 2 * c) * ROWS + r]).x);
-#pragma unroll 4
-          for (int64_t c = c0; c <= c1; ++c) {
-            const int64_t at = (c == c0 ? s0 : 2 * c) * ROWS + r;
-            const float2 y = __ldcg(&p.part_ml[at]);
-            const float4 a = __ldcg(reinterpret_cast<const float4*>(p.part_o) + at * PER + 2 * e);
-            const float4 b = __ldcg(reinterpret_cast<const float4*>(p.part_o) + at * PER + 2 * e + 1);
-            const float w = y.x == -INFINITY ? 0.f : ex2_approx(y.x - M);
-            L = fmaf(y.y, w, L);
-            f[0] = fmaf(a.x, w, f[0]);
-            f[1] = fmaf(a.y, w, f[1]);
-            f[2] = fmaf(a.z, w, f[2]);
-            f[3] = fmaf(a.w, w, f[3]);
-            f[4] = fmaf(b.x, w, f[4]);
-            f[5] = fmaf(b.y, w, f[5]);
-            f[6] = fmaf(b.z, w, f[6]);
-            f[7] = fmaf(b.w, w, f[7]);
+#pragma unroll 8
+          for (int s = 0; s < parts; ++s) {
+            const float4* from = reinterpret_cast<const float4*>(
+                p.part_o + (static_cast<int64_t>(s == 0 ? s0 : 2 * (c0 + s)) * ROWS + r) * D + 8 * e);
+            const float4 u = __ldcg(from), v = __ldcg(from + 1);
+            const float a = wbuf[s * ROWS + r];
+            f[0] = fmaf(u.x, a, f[0]);
+            f[1] = fmaf(u.y, a, f[1]);
+            f[2] = fmaf(u.z, a, f[2]);
+            f[3] = fmaf(u.w, a, f[3]);
+            f[4] = fmaf(v.x, a, f[4]);
+            f[5] = fmaf(v.y, a, f[5]);
+            f[6] = fmaf(v.z, a, f[6]);
+            f[7] = fmaf(v.w, a, f[7]);
           }
+          if (row < R) store_row<D, BF16>(p, it.seq, it.kvh, row, 8 * e, f, 1.f);
         }
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float a = f[2 * k] * inv, b = f[2 * k + 1] * inv;
-          if constexpr (BF16) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-            w[k] = *reinterpret_cast<const uint32_t*>(&h);
-          } else {
-            w[k] = pack_f16(a, b);
-          }
-        }
-        const int qi = row / p.g, h = it.kvh * p.g + row % p.g;
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + it.seq * p.o_st[0] + qi * p.o_st[1] + h * p.o_st[2] +
-                                  8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (e == 0)
-          p.lse[(static_cast<int64_t>(it.seq) * p.hq + h) * p.sq + qi] =
-              L > 0.f ? (M + lg2_approx(L)) * kLn2 : -INFINITY;
       }
     }
-    item_at += it.n;
-    live = cw.next(p);
     if (live) __syncthreads();  // the buffers are free again
   }
 }
@@ -804,6 +877,7 @@ cudaError_t launch_dtype(const Attend4Params& p, int dtype, int sms, Attend4Plan
   if (plan != nullptr) {
     plan->rows = C::ROWS;
     plan->block = C::BK;
+    plan->gap = kGap;
     plan->max_ctas = sms * C::CTAS;
     return cudaSuccess;
   }

@@ -108,9 +108,10 @@ struct Attend4Params {
   int* status;
 };
 
-// The kernel a call takes: query rows of a tile, keys of a block, CTAs of a full grid.
+// The kernel a call takes: query rows of a tile, keys of a block, blocks that an item costs
+// besides its own, CTAs of a full grid.
 struct Attend4Plan {
-  int rows, block, max_ctas;
+  int rows, block, gap, max_ctas;
 };
 
 // dtype 0 = bf16, 1 = fp16.

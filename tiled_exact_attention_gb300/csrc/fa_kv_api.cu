@@ -171,10 +171,10 @@ bool plan_attend(const fa_kvcache_int4_args* a, int sms, AttendWork* w) {
   w->ntiles = static_cast<int>((rows + w->plan.rows - 1) / w->plan.rows);
   // no more CTAs than blocks there could be (a block table's row is the longest sequence)
   const double blocks = static_cast<double>(a->b) * a->hkv * w->ntiles *
-                        (static_cast<double>(a->block_table_stride) * a->page_size / w->plan.block + 1.0);
+                        (static_cast<double>(a->block_table_stride) * a->page_size / w->plan.block + 1.0 + w->plan.gap);
   w->grid = blocks < w->plan.max_ctas ? static_cast<int>(blocks) : w->plan.max_ctas;
   if (w->grid < 1) w->grid = 1;
-  if (blocks / w->grid > 1e9) return false;  // (a CTA counts its blocks in 32 bits)
+  if (blocks > 2e9) return false;  // (counted in 32 bits: 2^36 keys over all KV heads and row tiles)
   w->o_bytes = round256(static_cast<size_t>(2) * w->grid * w->plan.rows * a->d * sizeof(float));
   w->ml_bytes = round256(static_cast<size_t>(2) * w->grid * w->plan.rows * sizeof(float2));
   w->bytes = w->o_bytes + w->ml_bytes + round256(static_cast<size_t>(w->grid) * sizeof(int));
