@@ -36,16 +36,10 @@
 namespace fa {
 namespace attend4 {
 
-#ifndef A4_WARPS
-#define A4_WARPS 4
-#endif
-#ifndef A4_GAP
-#define A4_GAP 12
-#endif
-constexpr int kWarps = A4_WARPS;
+constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kGap = A4_GAP;        // what an item costs besides its blocks, in blocks
-constexpr int kMinShare = 8 + kGap;  // a CTA's stretch of the line at least ...
+constexpr int kGap = 12;            // what an item costs besides its blocks, in blocks
+constexpr int kMinShare = 4 + kGap;  // a CTA's stretch of the line at least ...
 constexpr int kUncut = 16;      // ... and items of up to so many blocks are never cut
 constexpr int kMostParts = 64;  // CTAs that share an item at most
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -54,7 +48,7 @@ enum : int { kSiteFull = 48 };
 
 template <int D, int NG, int NT>
 struct Cfg {
-  static constexpr int UNITS = D == 256 || (kWarps == 8 && NT == 2) ? 1 : 2;  // units per block (a block lies in one page)
+  static constexpr int UNITS = D == 256 ? 1 : 2;  // units per block (a block lies in one page)
   static constexpr int BK = UNITS * kKv4Unit;     // keys per block
   static constexpr int UB = kv4_unit_bytes(D, NG);
   static constexpr int STAGE = UNITS * UB;
@@ -64,7 +58,7 @@ struct Cfg {
   static constexpr int OP = DP + 4;             // pitch of a row there (floats)
   static constexpr int RING = kWarps * STAGES * STAGE;
   static constexpr int SMEM = RING + kWarps * ROWS * OP * 4 + kWarps * ROWS * 8 + kWarps * STAGES * 8 + 16;
-  static constexpr int CTAS = kWarps == 8 ? 1 : NT == 1 && SMEM <= 74 * 1024 ? 3 : (SMEM <= 112 * 1024 ? 2 : 1);  // per SM
+  static constexpr int CTAS = NT == 1 && SMEM <= 74 * 1024 ? 3 : (SMEM <= 112 * 1024 ? 2 : 1);  // per SM
   static constexpr bool ONES = NG <= 2 || (NG == 4 && NT == 1);
   static_assert(kMostParts * ROWS * 4 <= kWarps * ROWS * OP * 4, "the merge's weights fit the exchange buffer");
 };
@@ -93,6 +87,15 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same into a fresh accumulator.
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -329,62 +332,42 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
   };
   load_q();
 
-  // ---- the warp's stream of blocks: `pw` runs ahead of the consumer, and the page of
-  // the block after the copies in flight is on its way from the block table
+  // ---- the warp's stream of blocks: `pw` runs ahead of the consumer by batches of up
+  // to 32 blocks of an item.  Lane i holds where block i of the batch lies and copies it.
   Walk<BK, ROWS> pw = cw;
-  int pu = pw.u0 + warp, prow = 0;  // the block after the next, and its row in its page
-  const int* ptable = nullptr;      // ... and its table entry
-  struct Next {
-    int page;  // -1: no block is left
-    int64_t off;
-  };
-  auto place = [&]() {
-    const int key = (pw.it.blo + pu) * BK, page = key / p.page_size;
-    prow = key - page * p.page_size;
-    ptable = p.block_table + pw.it.seq * p.bt_stride + page;
-  };
+  int pu = pw.u0 + warp, batch = 0, next = 0;  // the batch after this one; blocks in it; the next to copy
+  int page = 0;
+  int64_t off = 0;
   bool more = true;
-  auto seek = [&](bool fresh) {
+  auto refill = [&]() {
     while (more && (pu >= pw.ue || pw.it.hi <= pw.it.lo)) {
       more = pw.next(p);
       pu = pw.u0 + warp;
-      fresh = true;
     }
-    Next n{0, -1};
+    next = batch = 0;
     if (more) {
-      if (fresh) place();
-      n.page = *ptable;
-      n.off = pw.it.kvh * p.c_st[1] + (prow / kKv4Unit) * C::UB;
-      pu += kWarps;
-      prow += kWarps * BK;
-      while (prow >= p.page_size) {
-        prow -= p.page_size;
-        ++ptable;
+      batch = min(32, (pw.ue - pu + kWarps - 1) / kWarps);
+      const int key = (pw.it.blo + pu + lane * kWarps) * BK, at = key / p.page_size;
+      if (lane < batch) page = p.block_table[pw.it.seq * p.bt_stride + at];
+      off = pw.it.kvh * p.c_st[1] + ((key - at * p.page_size) / kKv4Unit) * C::UB;
+      pu += 32 * kWarps;
+    }
+  };
+  auto copy_next = [&](int slot) {
+    if (batch == 0) return;
+    if (lane == next) {
+      if (page < 0 || page >= p.num_pages) {
+        record_error(p.status, kErrDeviceArg);
+        page = 0;
       }
-    }
-    return n;
-  };
-  auto copy = [&](const Next& n, int slot) {
-    int page = n.page;
-    if (page < 0 || page >= p.num_pages) {
-      record_error(p.status, kErrDeviceArg);
-      page = 0;
-    }
-    if (lane == 0) {
       mbar_arrive_expect_tx(&full[slot], C::STAGE);
-      bulk_load(ring + slot * C::STAGE, p.cache + page * p.c_st[0] + n.off, C::STAGE, &full[slot]);
+      bulk_load(ring + slot * C::STAGE, p.cache + page * p.c_st[0] + off, C::STAGE, &full[slot]);
     }
+    if (++next == batch) refill();
   };
-  Next next;
-  {
-    Next first[C::STAGES];
-#pragma unroll
-    for (int s = 0; s < C::STAGES; ++s) first[s] = seek(s == 0);
-    next = seek(false);
-#pragma unroll
-    for (int s = 0; s < C::STAGES; ++s)
-      if (first[s].off >= 0) copy(first[s], s);
-  }
+  refill();
+#pragma unroll 1
+  for (int s = 0; s < C::STAGES; ++s) copy_next(s);
   int slot = 0;
   uint32_t phase = 0;
 
@@ -491,17 +474,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
 #pragma unroll
             for (int j = 0; j < J; ++j) {
               const int w = c * J + j;
-              if (w % GW == 0) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
-              }
               const uint32_t ha = wa[j] >> 8, hb = wb[j] >> 8;
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                mma16816(acc[nt], wa[j] & 0x000f000fu, wb[j] & 0x000f000fu, ha & 0x000f000fu, hb & 0x000f000fu,
-                         qf[w][0][nt][0], qf[w][0][nt][1]);
+                if (w % GW == 0)
+                  mma16816_first(acc[nt], wa[j] & 0x000f000fu, wb[j] & 0x000f000fu, ha & 0x000f000fu, hb & 0x000f000fu,
+                                 qf[w][0][nt][0], qf[w][0][nt][1]);
+                else
+                  mma16816(acc[nt], wa[j] & 0x000f000fu, wb[j] & 0x000f000fu, ha & 0x000f000fu, hb & 0x000f000fu,
+                           qf[w][0][nt][0], qf[w][0][nt][1]);
                 mma16816(acc[nt], wa[j] & 0x00f000f0u, wb[j] & 0x00f000f0u, ha & 0x00f000f0u, hb & 0x00f000f0u,
                          qf[w][1][nt][0], qf[w][1][nt][1]);
               }
@@ -694,10 +675,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
           }
         }
         __syncwarp();  // every lane has read the stage
-        if (next.off >= 0) {
-          copy(next, slot);
-          next = seek(false);
-        }
+        copy_next(slot);
         if (++slot == C::STAGES) {
           slot = 0;
           phase ^= 1u;
@@ -797,6 +775,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
       // the last of the item's CTAs to get here joins the parts (the barrier puts the
       // CTA's stores before thread 0's releasing and acquiring count)
       __syncthreads();
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zeroed by the grid before
       if (threadIdx.x == 0) *last_in = count_in(p.counters + c0) == c1 - c0;
       __syncthreads();
       if (*last_in) {
@@ -854,10 +833,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
   }
 }
 
-// CTAs of a full grid, and the bytes of its partials.
-template <int D, int NG, int NT>
-constexpr int ctas_per_sm() {
-  return Cfg<D, NG, NT>::CTAS;
+static __global__ void zero_counters_kernel(int* counters, int n) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int i = threadIdx.x; i < n; i += blockDim.x) counters[i] = 0;
 }
 
 template <int D, int NG, bool BF16, int NT>
@@ -867,8 +845,24 @@ cudaError_t launch_one(const Attend4Params& p, int grid, cudaStream_t stream) {
   static_assert(C::SMEM <= 227 * 1024, "shared memory");
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  k<<<grid, kThreads, C::SMEM, stream>>>(p);
-  return cudaGetLastError();
+  if (!p.cuts) {
+    k<<<grid, kThreads, C::SMEM, stream>>>(p);
+    return cudaGetLastError();
+  }
+  // the kernel starts beside the one that zeroes its counters and waits for it only
+  // before it counts
+  zero_counters_kernel<<<1, 512, 0, stream>>>(p.counters, grid);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, p);
 }
 
 template <int D, int NG, int NT>
@@ -878,6 +872,7 @@ cudaError_t launch_dtype(const Attend4Params& p, int dtype, int sms, Attend4Plan
     plan->rows = C::ROWS;
     plan->block = C::BK;
     plan->gap = kGap;
+    plan->uncut = kUncut;
     plan->max_ctas = sms * C::CTAS;
     return cudaSuccess;
   }

@@ -90,6 +90,7 @@ struct Attend4Params {
   int b, sq, hq, hkv, g, d, group;
   int ntiles;     // row tiles of a KV head: ceil(sq * g / rows of a tile)
   int grid;       // CTAs
+  int cuts;       // 0: no item can be long enough to be cut
   const uint8_t* cache;
   int64_t c_st[2];
   int num_pages, page_size;
@@ -100,8 +101,8 @@ struct Attend4Params {
   float scale_log2;  // scale * log2(e)
   float sc_k, sc_b;  // softcap as in DecodeParams (sc_b = 0: off)
   // Partials of items that several CTAs share, two slots a CTA: O before the division
-  // [2 grid][rows][d], its maximum and sum [2 grid][rows]; counters [grid], zero at
-  // launch, one for the item that starts in a CTA's stretch and leaves it.
+  // [2 grid][rows][d], its maximum and sum [2 grid][rows]; counters [grid], zeroed by
+  // the launch, one for the item that starts in a CTA's stretch and leaves it.
   float* part_o;
   float2* part_ml;
   int* counters;
@@ -109,9 +110,9 @@ struct Attend4Params {
 };
 
 // The kernel a call takes: query rows of a tile, keys of a block, blocks that an item costs
-// besides its own, CTAs of a full grid.
+// besides its own, blocks of an item that is never cut, CTAs of a full grid.
 struct Attend4Plan {
-  int rows, block, gap, max_ctas;
+  int rows, block, gap, uncut, max_ctas;
 };
 
 // dtype 0 = bf16, 1 = fp16.

@@ -292,9 +292,8 @@ fa_status fa_fwd_kvcache_int4(const fa_kvcache_int4_args* a, void* workspace, si
     p.sc_k = static_cast<float>(2.0 / static_cast<double>(a->softcap));
     p.sc_b = static_cast<float>(static_cast<double>(a->softcap) * 1.4426950408889634);
   }
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(p.counters, 0, static_cast<size_t>(w.grid) * sizeof(int), st) != cudaSuccess) return FA_ERR_CUDA;
-  return attend(p, a->dtype, sms, nullptr, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  p.cuts = static_cast<int64_t>(a->block_table_stride) * a->page_size > static_cast<int64_t>(w.plan.uncut) * w.plan.block;
+  return attend(p, a->dtype, sms, nullptr, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"
