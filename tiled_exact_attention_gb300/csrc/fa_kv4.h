@@ -50,6 +50,7 @@ struct KvAppendParams {
   const void* v;
   int64_t q_st[2], qo_st[2], k_st[2], v_st[2];
   int b, total, hq, hkv, d;
+  int parts;          // warps that share a token's rows
   const int* cu;      // [b + 1], or null: total / b tokens each
   const int* seqlens;  // [b] keys after the append
   const float* cos_sin;  // [max_positions][rot]: rot / 2 cosines, rot / 2 sines
@@ -71,6 +72,7 @@ struct KvGatherParams {
   const uint8_t* cache;
   int64_t c_st[2];
   int b, total, hkv, d, group, num_pages, page_size;
+  int parts;  // warps that share a token's heads
   const int* block_table;
   int64_t bt_stride;
   const int* seqlens;
@@ -116,8 +118,8 @@ struct Attend4Plan {
 };
 
 // dtype 0 = bf16, 1 = fp16.
-cudaError_t launch_kv_append(const KvAppendParams& p, int dtype, cudaStream_t stream);
-cudaError_t launch_kv_gather4(const KvGatherParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_kv_append(KvAppendParams& p, int dtype, int sms, cudaStream_t stream);  // (sets p.parts)
+cudaError_t launch_kv_gather4(KvGatherParams& p, int dtype, int sms, cudaStream_t stream);
 // With a plan: fill it from p.group, p.sq and p.g and launch nothing.
 cudaError_t attend4_d64(const Attend4Params& p, int dtype, int sms, Attend4Plan* plan, cudaStream_t stream);
 cudaError_t attend4_d128(const Attend4Params& p, int dtype, int sms, Attend4Plan* plan, cudaStream_t stream);

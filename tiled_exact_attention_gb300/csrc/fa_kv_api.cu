@@ -121,7 +121,7 @@ fa_status append(const fa_kv_append_args* a, bool int4, void* stream) {
   p.page_size = a->page_size;
   p.block_table = a->block_table;
   p.bt_stride = a->block_table_stride;
-  return launch_kv_append(p, a->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_kv_append(p, a->dtype, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status validate_attend(const fa_kvcache_int4_args* a) {
@@ -234,7 +234,7 @@ fa_status fa_kv_gather_int4(const fa_kv_gather_int4_args* a, void* stream) {
   p.cu = a->cu_seqlens;
   p.k = a->k;
   p.v = a->v;
-  return launch_kv_gather4(p, a->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_kv_gather4(p, a->dtype, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 size_t fa_kvcache_int4_workspace_size(const fa_kvcache_int4_args* a) {
