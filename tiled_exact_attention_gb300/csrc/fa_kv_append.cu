@@ -45,6 +45,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return x;
 }
 
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+  uint64_t x;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
+  return x;
+}
+
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t x;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(a), "l"(b), "l"(c));
@@ -87,22 +93,23 @@ __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
   }
 }
 
-// Sixteen dims of a row.
-struct Row16 {
-  uint4 a, b;
-  __device__ __forceinline__ uint32_t word(int i) const {  // (i is a constant once unrolled)
-    switch (i) {
-      case 0: return a.x;
-      case 1: return a.y;
-      case 2: return a.z;
-      case 3: return a.w;
-      case 4: return b.x;
-      case 5: return b.y;
-      case 6: return b.z;
-      default: return b.w;
-    }
-  }
+// Eight 16-bit dims of a row.
+struct Chunk {
+  uint32_t w[4];
 };
+
+__device__ __forceinline__ Chunk load_chunk(const uint16_t* p) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  return Chunk{{u.x, u.y, u.z, u.w}};
+}
+
+__device__ __forceinline__ void store_chunk(uint16_t* p, const Chunk& c) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
+}
+
+// The two chunks of a row (of D / 8) that lane k of its D / 16 lanes holds, in the
+// order of the 4-bit cache: its codes of K are one 64-bit word, those of V two.
+__device__ __forceinline__ int cache_chunk(int k, int which) { return 8 * (k / 4) + k % 4 + 4 * which; }
 
 // A token's place: sequence, position, page and row.  ok = false: it has none (a row
 // of no sequence, a padding token, or an argument that fails its check).
@@ -170,226 +177,316 @@ __device__ __forceinline__ void check_prefix(const int* cu, int b, int total, in
   if (!ok) record_error(status, kErrDeviceArg);
 }
 
-// The rotation of a lane's sixteen dims (two chunks of eight).  Every pair of
-// neighbouring dims becomes x * c + o * s with the dims o that they turn with (those of
-// the chunk R / 2 away, or, interleaved, the same two exchanged) and the sign in s:
-// each product and the sum rounded once (no contraction), as in the plain formula.
+// The rotation of a lane's two chunks.  Half-split: dims [8 c, 8 c + 8) turn with dims
+// R / 2 further on, and the lane holds both chunks, so no row is read twice and the
+// eight cosines and sines serve both.  Interleaved: a chunk holds four pairs that turn
+// in themselves.  Products and sums are rounded one by one, as in the plain formula.
 struct Turn {
-  uint64_t c[8], s[8];
-  bool on[2];     // the chunk is rotated
-  int other[2];   // half-split: first dim of the chunk it turns with
+  float c[8], s[8];  // half-split: of the eight angles; interleaved: of the chunks' four each
+  bool on[2];
+  bool split;
 };
 
 template <bool BF16>
-__device__ __forceinline__ Row16 turn(const Row16& x, const Row16& o, const Turn& t, bool interleaved) {
-  uint32_t w[8];
+__device__ __forceinline__ void turn(Chunk (&x)[2], const Turn& t) {
+  if (t.split) {
+    if (!t.on[0]) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    w[i] = x.word(i);
-    if (t.on[i / 4]) {
-      const uint64_t v = widen2<BF16>(w[i]);
-      const float2 p = unpack2(v);
-      const uint64_t u = interleaved ? pack2(p.y, p.x) : widen2<BF16>(o.word(i));
-      const float2 y = unpack2(add2(mul2(v, t.c[i]), mul2(u, t.s[i])));
-      w[i] = narrow2<BF16>(y.x, y.y);
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t a = widen2<BF16>(x[0].w[i]), b = widen2<BF16>(x[1].w[i]);
+      const uint64_t c = pack2(t.c[2 * i], t.c[2 * i + 1]), s = pack2(t.s[2 * i], t.s[2 * i + 1]);
+      const float2 ya = unpack2(sub2(mul2(a, c), mul2(b, s))), yb = unpack2(add2(mul2(b, c), mul2(a, s)));
+      x[0].w[i] = narrow2<BF16>(ya.x, ya.y);
+      x[1].w[i] = narrow2<BF16>(yb.x, yb.y);
     }
+    return;
   }
-  return Row16{make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7])};
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    if (t.on[q]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = unpack2(widen2<BF16>(x[q].w[i]));
+        const float c = t.c[4 * q + i], s = t.s[4 * q + i];
+        x[q].w[i] = narrow2<BF16>(__fsub_rn(__fmul_rn(v.x, c), __fmul_rn(v.y, s)),
+                                  __fadd_rn(__fmul_rn(v.y, c), __fmul_rn(v.x, s)));
+      }
+    }
 }
 
-// Sixteen 16-bit values quantised with the other lanes of their group (group / 16
-// lanes): codes (nibble i of a word: value i) and the (scale, min) pair as stored.
-// The minimum is exact in the rows' type; the scale (max - min) / 15 is rounded to it
-// (halved first, so that it cannot overflow).  Many 16-bit values lie exactly between
-// two levels, so the quotient (x - min) / scale has to be the correctly rounded one:
-// x times the reciprocal, then one correction by its exact remainder (Markstein).
-// Codes are taken from the sum with 1.5 * 2^23, whose low bits are the nearest integer.
+// The smallest value of a chunk and of its negative, in one word.
 template <bool BF16>
-__device__ __forceinline__ void quantise16(const Row16& x, int lanes, uint32_t (&codes)[2], uint32_t* pair) {
-  // minimum of the values and of their negatives, two and two, then both in one word
-  uint32_t mn = x.word(0), mx = x.word(0) ^ 0x80008000u;
-#pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    mn = min2<BF16>(mn, x.word(i));
-    mx = min2<BF16>(mx, x.word(i) ^ 0x80008000u);
-  }
-  uint32_t both = min2<BF16>(__byte_perm(mn, mx, 0x5410), __byte_perm(mn, mx, 0x7632));
-  for (int s = 1; s < lanes; s *= 2) both = min2<BF16>(both, __shfl_xor_sync(0xffffffffu, both, s));
-  const float low = widen1<BF16>(both & 0xffffu), neg_high = widen1<BF16>(both >> 16);
-  const float half_range = __fsub_rn(-0.5f * neg_high, 0.5f * low);
-  const float by = 0x1.111112p-3f;  // 1 / 7.5 to nearest
+__device__ __forceinline__ uint32_t extremes(const Chunk& x) {
+  const uint32_t mn = min2<BF16>(min2<BF16>(x.w[0], x.w[1]), min2<BF16>(x.w[2], x.w[3]));
+  const uint32_t neg = 0x80008000u;
+  const uint32_t mx = min2<BF16>(min2<BF16>(x.w[0] ^ neg, x.w[1] ^ neg), min2<BF16>(x.w[2] ^ neg, x.w[3] ^ neg));
+  return min2<BF16>(__byte_perm(mn, mx, 0x5410), __byte_perm(mn, mx, 0x7632));
+}
+
+// The levels of a group from its extremes: the (scale, min) pair as stored, and what
+// the codes are computed with.  The minimum is exact in the rows' type; the scale
+// (max - min) / 15 is rounded to it (halved first, so that it cannot overflow).
+struct Levels {
+  uint32_t pair;
+  float low, s, r;
+};
+
+template <bool BF16>
+__device__ __forceinline__ Levels levels(uint32_t both) {
+  Levels v;
+  v.low = widen1<BF16>(both & 0xffffu);
+  const float half_range = __fsub_rn(-0.5f * widen1<BF16>(both >> 16), 0.5f * v.low);
+  const float by = 0x1.111112p-3f;  // 1 / 7.5 to nearest; the quotient is corrected as below
   float q = __fmul_rn(half_range, by);
   q = __fmaf_rn(__fmaf_rn(-7.5f, q, half_range), by, q);
-  uint32_t sm = narrow2<BF16>(q, low);
-  float s = widen1<BF16>(sm & 0xffffu);
-  if (s < 0x1p-100f) {
-    s = 0.f;
-    sm &= 0xffff0000u;
+  v.pair = narrow2<BF16>(q, v.low);
+  v.s = widen1<BF16>(v.pair & 0xffffu);
+  if (v.s < 0x1p-100f) {
+    v.s = 0.f;
+    v.pair &= 0xffff0000u;
   }
-  *pair = sm;
-  const float r = s > 0.f ? __frcp_rn(s) : 0.f;
-  const uint64_t r2 = pack2(r, r), s2 = pack2(-s, -s), m2 = pack2(-low, -low);
+  v.r = v.s > 0.f ? __frcp_rn(v.s) : 0.f;
+  return v;
+}
+
+// The codes of a chunk, value i in nibble i.  Many 16-bit values lie exactly between
+// two levels, so the quotient (x - min) / scale has to be the correctly rounded one:
+// x times the reciprocal, then one correction by its exact remainder (Markstein).  The
+// nearest integer is in the low bits of its sum with 1.5 * 2^23.
+template <bool BF16>
+__device__ __forceinline__ uint32_t quantise(const Chunk& x, const Levels& v) {
+  const uint64_t r2 = pack2(v.r, v.r), s2 = pack2(-v.s, -v.s), m2 = pack2(-v.low, -v.low);
   const uint64_t magic = pack2(12582912.f, 12582912.f);
+  uint32_t word = 0;
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    uint32_t word = 0;
-#pragma unroll
-    for (int i = 3; i >= 0; --i) {
-      const uint64_t a = add2(widen2<BF16>(x.word(4 * c + i)), m2);
-      uint64_t y = mul2(a, r2);
-      y = fma2(fma2(s2, y, a), r2, y);
-      if (!BF16 && s < 0x1p-14f) {  // a subnormal scale may be far too small
-        const float2 f = unpack2(y);
-        y = pack2(fminf(f.x, 15.f), fminf(f.y, 15.f));
-      }
-      const float2 z = unpack2(add2(y, magic));  // bits 0x4b400000 + code
-      word = (word << 4) + __float_as_uint(z.y);
-      word = (word << 4) + __float_as_uint(z.x);
+  for (int i = 3; i >= 0; --i) {
+    const uint64_t a = add2(widen2<BF16>(x.w[i]), m2);
+    uint64_t y = mul2(a, r2);
+    y = fma2(fma2(s2, y, a), r2, y);
+    if (!BF16 && v.s < 0x1p-14f) {  // a subnormal scale may be far too small
+      const float2 f = unpack2(y);
+      y = pack2(fminf(f.x, 15.f), fminf(f.y, 15.f));
     }
-    codes[c] = word - 0x3f400000u;  // the sum of 0x4b400000 << 4 i, i = 0..7
+    const float2 z = unpack2(add2(y, magic));  // bits 0x4b400000 + code
+    word = (word << 4) + __float_as_uint(z.y);
+    word = (word << 4) + __float_as_uint(z.x);
+  }
+  return word - 0x3f400000u;  // the sum of 0x4b400000 << 4 i, i = 0..7
+}
+
+// Both chunks of a lane (in the cache's order) quantised in groups of `group` dims; the
+// four or eight lanes of a group take part.  pair[1] is the second chunk's.
+template <bool BF16>
+__device__ __forceinline__ void quantise_row(const Chunk (&x)[2], int group, uint32_t (&codes)[2], uint32_t (&pair)[2]) {
+  uint32_t e0 = extremes<BF16>(x[0]), e1 = extremes<BF16>(x[1]);
+  if (group == 32) {
+#pragma unroll
+    for (int s = 1; s < 4; s *= 2) {
+      e0 = min2<BF16>(e0, __shfl_xor_sync(0xffffffffu, e0, s));
+      e1 = min2<BF16>(e1, __shfl_xor_sync(0xffffffffu, e1, s));
+    }
+    const Levels v0 = levels<BF16>(e0), v1 = levels<BF16>(e1);
+    codes[0] = quantise<BF16>(x[0], v0);
+    codes[1] = quantise<BF16>(x[1], v1);
+    pair[0] = v0.pair;
+    pair[1] = v1.pair;
+  } else {
+    e0 = min2<BF16>(e0, e1);
+    for (int s = 1; s < group / 16; s *= 2) e0 = min2<BF16>(e0, __shfl_xor_sync(0xffffffffu, e0, s));
+    const Levels v = levels<BF16>(e0);
+    codes[0] = quantise<BF16>(x[0], v);
+    codes[1] = quantise<BF16>(x[1], v);
+    pair[0] = pair[1] = v.pair;
   }
 }
 
 template <int D, bool BF16, bool INT4>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
+__global__ void __launch_bounds__(kThreads, INT4 ? 5 : 6) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
   constexpr int LPT = D / 16, TPW = 32 / LPT;  // lanes of a token, tokens of a warp
-  constexpr int U = 2;                         // rows in flight
+  constexpr int U = 4;                         // rows in flight
   check_prefix(p.cu, p.b, p.total, p.status);
   const int lane = threadIdx.x & 31, k = lane % LPT;
   const unsigned w = (blockIdx.x * kThreads + threadIdx.x) >> 5;
-  const int part = static_cast<int>(w % p.parts);  // this warp's heads: part, part + parts, ...
-  const unsigned tok_u = (w / p.parts) * TPW + lane / LPT;
+  const int parts = p.parts, part = static_cast<int>(w % parts);  // this warp's rows: part, part + parts, ...
+  const unsigned tok_u = (w / parts) * TPW + lane / LPT;
   const int tok = static_cast<int>(min(tok_u, 0x7fffffffu));
   const bool live = tok < p.total;
-  const int heads = p.hq + 2 * p.hkv, turned = p.hq + p.hkv;
 
-  auto row_of = [&](int h) {
-    const uint16_t* x;
-    if (h < p.hq) x = static_cast<const uint16_t*>(p.q) + tok * p.q_st[0] + h * p.q_st[1];
-    else if (h < turned) x = static_cast<const uint16_t*>(p.k) + tok * p.k_st[0] + (h - p.hq) * p.k_st[1];
-    else x = static_cast<const uint16_t*>(p.v) + tok * p.v_st[0] + (h - turned) * p.v_st[1];
-    return x;
-  };
-  auto load16 = [&](const uint16_t* x) {
-    return Row16{*reinterpret_cast<const uint4*>(x), *reinterpret_cast<const uint4*>(x + 8)};
-  };
-
-  // ---- what the chunks turn with (known before the place is)
+  // ---- the lane's chunks of rows that turn: the cache's, or a chunk and its partner
   Turn t;
-  const int half = p.rot / 2;
-  const bool split = p.rot > 0 && !p.interleaved;
+  t.split = p.rot > 0 && !p.interleaved;
+  int ca = cache_chunk(k, 0), cb = cache_chunk(k, 1);
+  int from[2], slot[2];  // half-split: the lane, and which of its chunks, that has the cache's chunk
+  if (t.split) {
+    const int nr = p.rot / 16;
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const int dim = 16 * k + 8 * c;
-    t.on[c] = dim < p.rot;
-    t.other[c] = !t.on[c] || !split ? dim : (dim < half ? dim + half : dim - half);
+    for (int c = 0; c < 2; ++c) {
+      const int want = cache_chunk(k, c);
+      from[c] = want < nr ? want : (want < 2 * nr ? want - nr : nr + (want - 2 * nr) / 2);
+      slot[c] = want < nr ? 0 : (want < 2 * nr ? 1 : want % 2);
+      from[c] += lane - k;
+    }
+    ca = k < nr ? k : 2 * k;
+    cb = k < nr ? k + nr : 2 * k + 1;
+    t.on[0] = t.on[1] = k < nr;
+  } else {
+    t.on[0] = 8 * ca < p.rot;
+    t.on[1] = 8 * cb < p.rot;
   }
-  Row16 x[U], o[U];
-  auto load_rows = [&](int h0) {
+
+  // Rows h = part, part + parts, ... of one tensor, U at a time; the first are loaded
+  // before the token's place is known.
+  auto load_rows = [&](Chunk (&x)[U][2], const uint16_t* base, int64_t step, int h0, int n, int c0, int c1) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * p.parts;
-      if (live && h < heads) {
-        const uint16_t* row = row_of(h);
-        x[u] = load16(row + 16 * k);
-        if (split && h < turned)
-          o[u] = Row16{*reinterpret_cast<const uint4*>(row + t.other[0]), *reinterpret_cast<const uint4*>(row + t.other[1])};
+      const int h = h0 + u * parts;
+      if (live && h < n) {
+        x[u][0] = load_chunk(base + h * step + 8 * c0);
+        x[u][1] = load_chunk(base + h * step + 8 * c1);
       } else {
-        x[u] = o[u] = Row16{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+        x[u][0] = x[u][1] = Chunk{{0u, 0u, 0u, 0u}};
       }
     }
   };
-  load_rows(part);
+  const uint16_t* q_at = static_cast<const uint16_t*>(p.q) + tok * p.q_st[0];
+  const uint16_t* k_at = static_cast<const uint16_t*>(p.k) + tok * p.k_st[0];
+  const uint16_t* v_at = static_cast<const uint16_t*>(p.v) + tok * p.v_st[0];
+  const int k_first = (part + parts - p.hq % parts) % parts;              // rows are dealt over q, k and v in turn
+  const int v_first = (part + parts - (p.hq + p.hkv) % parts) % parts;
+  Chunk x[U][2];
+  if (part < p.hq) load_rows(x, q_at, p.q_st[1], part, p.hq, ca, cb);
   const Slot s = find_slot<LPT>(p.cu, p.b, p.total, p.seqlens, p.block_table, p.bt_stride, p.page_size, p.num_pages,
                                 p.rot > 0 ? p.max_positions : 0, tok, p.status);
-  {
-    const float* cs = p.cos_sin + static_cast<int64_t>(s.pos) * p.rot;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      t.c[i] = t.s[i] = 0;
-      if (s.ok && t.on[i / 4]) {
-        if (p.interleaved) {
-          const int a = 8 * k + i;
-          const float co = cs[a], si = cs[half + a];
-          t.c[i] = pack2(co, co);
-          t.s[i] = pack2(-si, si);
-        } else {
-          const int dim = 16 * k + 2 * i;
-          const bool low = dim < half;
-          const int a = low ? dim : dim - half;
-          const float2 co = *reinterpret_cast<const float2*>(cs + a), si = *reinterpret_cast<const float2*>(cs + half + a);
-          t.c[i] = pack2(co.x, co.y);
-          t.s[i] = low ? pack2(-si.x, -si.y) : pack2(si.x, si.y);
-        }
+  for (int i = 0; i < 8; ++i) t.c[i] = t.s[i] = 0.f;
+  if (s.ok) {
+    const float* cs = p.cos_sin + static_cast<int64_t>(s.pos) * p.rot;
+    const int half = p.rot / 2;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (t.on[q]) {
+        const int a = t.split ? 8 * ca + 4 * q : 4 * (q == 0 ? ca : cb);
+        const float2 c0 = *reinterpret_cast<const float2*>(cs + a), c1 = *reinterpret_cast<const float2*>(cs + a + 2);
+        const float2 s0 = *reinterpret_cast<const float2*>(cs + half + a);
+        const float2 s1 = *reinterpret_cast<const float2*>(cs + half + a + 2);
+        t.c[4 * q] = c0.x, t.c[4 * q + 1] = c0.y, t.c[4 * q + 2] = c1.x, t.c[4 * q + 3] = c1.y;
+        t.s[4 * q] = s0.x, t.s[4 * q + 1] = s0.y, t.s[4 * q + 2] = s1.x, t.s[4 * q + 3] = s1.y;
       }
-    }
-  }
-  const int ng = INT4 ? D / p.group : 1;
-  // 4-bit: a token and the one after it, both in this warp, share V's words if they
-  // are an even and an odd key of one sequence's page
-  const int r = s.row % kKv4Unit;
-  bool with_next = false, with_prev = false;
-  if constexpr (INT4) {
-    const int np = __shfl_down_sync(0xffffffffu, s.ok ? s.page : -1, LPT), nr = __shfl_down_sync(0xffffffffu, s.row, LPT);
-    with_next = s.ok && lane < 32 - LPT && s.row % 2 == 0 && np == s.page && nr == s.row + 1;
-    const int up = __shfl_up_sync(0xffffffffu, with_next ? 1 : 0, LPT);
-    with_prev = lane >= LPT && up != 0;
   }
 
-  for (int h0 = part; h0 < heads; h0 += U * p.parts) {
-    if (h0 != part) load_rows(h0);
+  // ---- queries
+  uint16_t* qo_at = static_cast<uint16_t*>(p.q_out) + tok * p.qo_st[0];
+  for (int h0 = part; h0 < p.hq; h0 += U * parts) {
+    if (h0 != part) load_rows(x, q_at, p.q_st[1], h0, p.hq, ca, cb);
     __syncwarp();  // (q_out may be q: a row is read before any lane writes it)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * p.parts;
-      if (h >= heads) break;
-      const bool is_q = h < p.hq, is_k = !is_q && h < turned;
-      const Row16 y = (is_q || is_k) && p.rot > 0 ? turn<BF16>(x[u], o[u], t, p.interleaved != 0) : x[u];
-      if (is_q) {
-        if (s.ok) {
-          uint16_t* dst = static_cast<uint16_t*>(p.q_out) + tok * p.qo_st[0] + h * p.qo_st[1] + 16 * k;
-          *reinterpret_cast<uint4*>(dst) = y.a;
-          *reinterpret_cast<uint4*>(dst + 8) = y.b;
-        }
-        continue;
+      const int h = h0 + u * parts;
+      if (h < p.hq && s.ok) {
+        turn<BF16>(x[u], t);
+        store_chunk(qo_at + h * p.qo_st[1] + 8 * ca, x[u][0]);
+        store_chunk(qo_at + h * p.qo_st[1] + 8 * cb, x[u][1]);
       }
-      const int kvh = is_k ? h - p.hq : h - turned;
-      if constexpr (!INT4) {
-        if (s.ok) {
-          uint16_t* dst = is_k ? static_cast<uint16_t*>(p.k_cache) + s.page * p.kc_st[0] + s.row * p.kc_st[1] + kvh * p.kc_st[2]
-                               : static_cast<uint16_t*>(p.v_cache) + s.page * p.vc_st[0] + s.row * p.vc_st[1] + kvh * p.vc_st[2];
-          *reinterpret_cast<uint4*>(dst + 16 * k) = y.a;
-          *reinterpret_cast<uint4*>(dst + 16 * k + 8) = y.b;
+    }
+  }
+
+  if constexpr (!INT4) {
+    uint16_t* kc_at = static_cast<uint16_t*>(p.k_cache) + s.page * p.kc_st[0] + s.row * p.kc_st[1];
+    for (int h0 = k_first; h0 < p.hkv; h0 += U * parts) {
+      load_rows(x, k_at, p.k_st[1], h0, p.hkv, ca, cb);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * parts;
+        if (h < p.hkv && s.ok) {
+          turn<BF16>(x[u], t);
+          store_chunk(kc_at + h * p.kc_st[2] + 8 * ca, x[u][0]);
+          store_chunk(kc_at + h * p.kc_st[2] + 8 * cb, x[u][1]);
         }
-      } else {
-        uint32_t codes[2], pair;
-        quantise16<BF16>(y, p.group / 16, codes, &pair);
-        uint8_t* unit = p.cache + s.page * p.c_st[0] + kvh * p.c_st[1] +
-                        static_cast<int64_t>(s.row / kKv4Unit) * kv4_unit_bytes(D, ng);
-        if (is_k) {
-          if (s.ok) {
-            uint32_t* kw = reinterpret_cast<uint32_t*>(unit);
-            kw[kv4_k_word(D, r, 2 * k)] = codes[0];
-            kw[kv4_k_word(D, r, 2 * k + 1)] = codes[1];
-          }
-        } else {
-          const uint32_t n0 = __shfl_down_sync(0xffffffffu, codes[0], LPT), n1 = __shfl_down_sync(0xffffffffu, codes[1], LPT);
-          uint16_t* vh = reinterpret_cast<uint16_t*>(unit + 16 * D);
-          if (with_next) {
-            uint32_t* vw = reinterpret_cast<uint32_t*>(vh);
-            vw[kv4_v_half(D, r, 4 * k) / 2] = __byte_perm(codes[0], n0, 0x5410);
-            vw[kv4_v_half(D, r, 4 * k + 1) / 2] = __byte_perm(codes[0], n0, 0x7632);
-            vw[kv4_v_half(D, r, 4 * k + 2) / 2] = __byte_perm(codes[1], n1, 0x5410);
-            vw[kv4_v_half(D, r, 4 * k + 3) / 2] = __byte_perm(codes[1], n1, 0x7632);
-          } else if (s.ok && !with_prev) {
-            vh[kv4_v_half(D, r, 4 * k)] = static_cast<uint16_t>(codes[0]);
-            vh[kv4_v_half(D, r, 4 * k + 1)] = static_cast<uint16_t>(codes[0] >> 16);
-            vh[kv4_v_half(D, r, 4 * k + 2)] = static_cast<uint16_t>(codes[1]);
-            vh[kv4_v_half(D, r, 4 * k + 3)] = static_cast<uint16_t>(codes[1] >> 16);
-          }
+      }
+    }
+    uint16_t* vc_at = static_cast<uint16_t*>(p.v_cache) + s.page * p.vc_st[0] + s.row * p.vc_st[1];
+    for (int h0 = v_first; h0 < p.hkv; h0 += U * parts) {
+      load_rows(x, v_at, p.v_st[1], h0, p.hkv, 2 * k, 2 * k + 1);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * parts;
+        if (h < p.hkv && s.ok) {
+          store_chunk(vc_at + h * p.vc_st[2] + 16 * k, x[u][0]);
+          store_chunk(vc_at + h * p.vc_st[2] + 16 * k + 8, x[u][1]);
         }
-        if (s.ok && k % (p.group / 16) == 0)
-          reinterpret_cast<uint32_t*>(unit + 32 * D)[(is_k ? 0 : 32 * ng) + r * ng + 16 * k / p.group] = pair;
+      }
+    }
+  } else {
+    const int ng = D / p.group, r = s.row % kKv4Unit;
+    const int g0 = 8 * cache_chunk(k, 0) / p.group, g1 = 8 * cache_chunk(k, 1) / p.group;
+    const bool tells = k % 4 == 0 && (p.group < 128 || k % 8 == 0);  // this lane stores its groups' pairs
+    uint8_t* unit0 = p.cache + s.page * p.c_st[0] + static_cast<int64_t>(s.row / kKv4Unit) * kv4_unit_bytes(D, ng);
+    auto store_pairs = [&](uint8_t* unit, bool of_v, const uint32_t (&pair)[2]) {
+      if (s.ok && tells) {
+        uint32_t* at = reinterpret_cast<uint32_t*>(unit + 32 * D) + (of_v ? 32 * ng : 0) + r * ng;
+        at[g0] = pair[0];
+        if (g1 != g0) at[g1] = pair[1];
+      }
+    };
+    for (int h0 = k_first; h0 < p.hkv; h0 += U * parts) {
+      load_rows(x, k_at, p.k_st[1], h0, p.hkv, ca, cb);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * parts;
+        if (h >= p.hkv) break;
+        turn<BF16>(x[u], t);
+        if (t.split) {  // to the cache's order
+          Chunk y[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t a = __shfl_sync(0xffffffffu, x[u][0].w[i], from[c]), b = __shfl_sync(0xffffffffu, x[u][1].w[i], from[c]);
+              y[c].w[i] = slot[c] ? b : a;
+            }
+          x[u][0] = y[0];
+          x[u][1] = y[1];
+        }
+        uint32_t codes[2], pair[2];
+        quantise_row<BF16>(x[u], p.group, codes, pair);
+        uint8_t* unit = unit0 + h * p.c_st[1];
+        if (s.ok)
+          *reinterpret_cast<uint2*>(reinterpret_cast<uint32_t*>(unit) + kv4_k_word(D, r, cache_chunk(k, 0))) =
+              make_uint2(codes[0], codes[1]);
+        store_pairs(unit, false, pair);
+      }
+    }
+    // a token and the one after it, both in this warp, share V's words if they are an
+    // even and an odd key of one page
+    const int np = __shfl_down_sync(0xffffffffu, s.ok ? s.page : -1, LPT), nr = __shfl_down_sync(0xffffffffu, s.row, LPT);
+    const bool with_next = s.ok && lane < 32 - LPT && s.row % 2 == 0 && np == s.page && nr == s.row + 1;
+    const int up = __shfl_up_sync(0xffffffffu, with_next ? 1 : 0, LPT);
+    const bool with_prev = lane >= LPT && up != 0;
+    const int quad = 2 * cache_chunk(k, 0);  // V's quads of the first chunk: this one and the next
+    for (int h0 = v_first; h0 < p.hkv; h0 += U * parts) {
+      load_rows(x, v_at, p.v_st[1], h0, p.hkv, cache_chunk(k, 0), cache_chunk(k, 1));
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * parts;
+        if (h >= p.hkv) break;
+        uint32_t codes[2], pair[2];
+        quantise_row<BF16>(x[u], p.group, codes, pair);
+        uint8_t* unit = unit0 + h * p.c_st[1];
+        const uint32_t n0 = __shfl_down_sync(0xffffffffu, codes[0], LPT), n1 = __shfl_down_sync(0xffffffffu, codes[1], LPT);
+        uint16_t* vh = reinterpret_cast<uint16_t*>(unit + 16 * D);
+        if (with_next) {  // (the words of the second chunk follow those of the first)
+          uint32_t* vw = reinterpret_cast<uint32_t*>(vh);
+          *reinterpret_cast<uint2*>(vw + kv4_v_half(D, r, quad) / 2) =
+              make_uint2(__byte_perm(codes[0], n0, 0x5410), __byte_perm(codes[1], n1, 0x5410));
+          *reinterpret_cast<uint2*>(vw + kv4_v_half(D, r, quad + 1) / 2) =
+              make_uint2(__byte_perm(codes[0], n0, 0x7632), __byte_perm(codes[1], n1, 0x7632));
+        } else if (s.ok && !with_prev) {
+          vh[kv4_v_half(D, r, quad)] = static_cast<uint16_t>(codes[0]);
+          vh[kv4_v_half(D, r, quad + 1)] = static_cast<uint16_t>(codes[0] >> 16);
+          vh[kv4_v_half(D, r, quad) + 2] = static_cast<uint16_t>(codes[1]);
+          vh[kv4_v_half(D, r, quad + 1) + 2] = static_cast<uint16_t>(codes[1] >> 16);
+        }
+        store_pairs(unit, true, pair);
       }
     }
   }
@@ -398,58 +495,68 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads) kv_gather4_kernel(const __grid_constant__ KvGatherParams p) {
   constexpr int LPT = D / 16, TPW = 32 / LPT;
-  constexpr int U = 2;
+  constexpr int U = 4;
   check_prefix(p.cu, p.b, p.total, p.status);
   const int lane = threadIdx.x & 31, k = lane % LPT;
   const unsigned w = (blockIdx.x * kThreads + threadIdx.x) >> 5;
-  const int part = static_cast<int>(w % p.parts);
-  const unsigned tok_u = (w / p.parts) * TPW + lane / LPT;
+  const int parts = p.parts, part = static_cast<int>(w % parts);
+  const unsigned tok_u = (w / parts) * TPW + lane / LPT;
   const int tok = static_cast<int>(min(tok_u, 0x7fffffffu));
   const Slot s = find_slot<LPT>(p.cu, p.b, p.total, p.seqlens, p.block_table, p.bt_stride, p.page_size, p.num_pages, 0,
                                 tok, p.status);
   if (!s.ok) return;
-  const int ng = D / p.group, r = s.row % kKv4Unit;
+  const int ng = D / p.group, r = s.row % kKv4Unit, chunk = cache_chunk(k, 0);
+  const int g0 = 8 * chunk / p.group, g1 = (8 * chunk + 32) / p.group;
   const uint8_t* base = p.cache + s.page * p.c_st[0] + static_cast<int64_t>(s.row / kKv4Unit) * kv4_unit_bytes(D, ng);
-  const uint32_t high = r % 2 != 0 ? 0x7632u : 0x5410u;  // the key's half of two words of V
-  for (int h0 = part; h0 < p.hkv; h0 += U * p.parts) {
-    uint32_t codes[U][2][2], pair[U][2];
+  const uint32_t mine = r % 2 != 0 ? 0x7632u : 0x5410u;  // the key's half of two words of V
+  uint16_t* to[2] = {static_cast<uint16_t*>(p.k) + tok * p.k_st[0] + 8 * chunk,
+                     static_cast<uint16_t*>(p.v) + tok * p.v_st[0] + 8 * chunk};
+  for (int h0 = part; h0 < p.hkv; h0 += U * parts) {
+    uint2 kw[U], v0[U], v1[U];
+    uint32_t pair[U][2][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * p.parts;
+      const int h = h0 + u * parts;
       if (h >= p.hkv) break;
       const uint8_t* unit = base + h * p.c_st[1];
-      const uint32_t* kw = reinterpret_cast<const uint32_t*>(unit);
       const uint32_t* vw = reinterpret_cast<const uint32_t*>(unit + 16 * D);
-      const uint32_t* par = reinterpret_cast<const uint32_t*>(unit + 32 * D) + r * ng + 16 * k / p.group;
-      codes[u][0][0] = kw[kv4_k_word(D, r, 2 * k)];
-      codes[u][0][1] = kw[kv4_k_word(D, r, 2 * k + 1)];
-      pair[u][0] = par[0];
-      pair[u][1] = par[32 * ng];
+      const uint32_t* par = reinterpret_cast<const uint32_t*>(unit + 32 * D) + r * ng;
+      kw[u] = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint32_t*>(unit) + kv4_k_word(D, r, chunk));
+      v0[u] = *reinterpret_cast<const uint2*>(vw + kv4_v_half(D, r, 2 * chunk) / 2);
+      v1[u] = *reinterpret_cast<const uint2*>(vw + kv4_v_half(D, r, 2 * chunk + 1) / 2);
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        codes[u][1][c] = __byte_perm(vw[kv4_v_half(D, r, 4 * k + 2 * c) / 2], vw[kv4_v_half(D, r, 4 * k + 2 * c + 1) / 2], high);
+      for (int kv = 0; kv < 2; ++kv) {
+        pair[u][kv][0] = par[kv * 32 * ng + g0];
+        pair[u][kv][1] = g1 == g0 ? pair[u][kv][0] : par[kv * 32 * ng + g1];
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * p.parts;
+      const int h = h0 + u * parts;
       if (h >= p.hkv) break;
+      const uint32_t codes[2][2] = {{kw[u].x, kw[u].y},
+                                    {__byte_perm(v0[u].x, v1[u].x, mine), __byte_perm(v0[u].y, v1[u].y, mine)}};
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        const float sc = widen1<BF16>(pair[u][kv] & 0xffffu), mn = widen1<BF16>(pair[u][kv] >> 16);
-        uint32_t out[8];
+        uint16_t* dst = to[kv] + h * (kv == 0 ? p.k_st[1] : p.v_st[1]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c) {
+          const float sc = widen1<BF16>(pair[u][kv][c] & 0xffffu), mn = widen1<BF16>(pair[u][kv][c] >> 16);
+          const uint64_t s2 = pack2(sc, sc), m2 = pack2(mn, mn), off = pack2(-1024.f, -1024.f);
+          // nibbles i and i + 4 of a word as the fp16 pair 1024 + code, then fp32; scale * code
+          // is exact, so the fused sum is min + scale * code rounded once
+          float f[8];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            // (scale * code is exact, so the fused sum is min + scale * code rounded once)
-            const uint32_t two = codes[u][kv][c] >> (8 * i);
-            const float a = static_cast<float>(two & 15u), b = static_cast<float>((two >> 4) & 15u);
-            out[4 * c + i] = narrow2<BF16>(__fmaf_rn(sc, a, mn), __fmaf_rn(sc, b, mn));
+            const uint32_t two = ((codes[kv][c] >> (4 * i)) & 0x000f000fu) | 0x64006400u;
+            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&two));
+            const float2 y = unpack2(fma2(s2, add2(pack2(x.x, x.y), off), m2));
+            f[i] = y.x;
+            f[i + 4] = y.y;
           }
-        uint16_t* dst = (kv == 0 ? static_cast<uint16_t*>(p.k) + tok * p.k_st[0] + h * p.k_st[1]
-                                 : static_cast<uint16_t*>(p.v) + tok * p.v_st[0] + h * p.v_st[1]) + 16 * k;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
-        *reinterpret_cast<uint4*>(dst + 8) = make_uint4(out[4], out[5], out[6], out[7]);
+          store_chunk(dst + 32 * c, Chunk{{narrow2<BF16>(f[0], f[1]), narrow2<BF16>(f[2], f[3]), narrow2<BF16>(f[4], f[5]),
+                                           narrow2<BF16>(f[6], f[7])}});
+        }
       }
     }
   }
