@@ -93,6 +93,17 @@ __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
   }
 }
 
+template <bool BF16>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 x = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&x);
+  } else {
+    const __half2 x = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&x);
+  }
+}
+
 // Eight 16-bit dims of a row.
 struct Chunk {
   uint32_t w[4];
@@ -214,12 +225,16 @@ __device__ __forceinline__ void turn(Chunk (&x)[2], const Turn& t) {
     }
 }
 
-// The smallest value of a chunk and of its negative, in one word.
+// The smallest value of one or both chunks, and of their negatives, in one word.
 template <bool BF16>
-__device__ __forceinline__ uint32_t extremes(const Chunk& x) {
-  const uint32_t mn = min2<BF16>(min2<BF16>(x.w[0], x.w[1]), min2<BF16>(x.w[2], x.w[3]));
-  const uint32_t neg = 0x80008000u;
-  const uint32_t mx = min2<BF16>(min2<BF16>(x.w[0] ^ neg, x.w[1] ^ neg), min2<BF16>(x.w[2] ^ neg, x.w[3] ^ neg));
+__device__ __forceinline__ uint32_t extremes(const Chunk* x, int n) {
+  uint32_t mn = x[0].w[0], mx = x[0].w[0];
+#pragma unroll
+  for (int i = 1; i < 4 * n; ++i) {
+    mn = min2<BF16>(mn, x[i / 4].w[i % 4]);
+    mx = max2<BF16>(mx, x[i / 4].w[i % 4]);
+  }
+  mx ^= 0x80008000u;
   return min2<BF16>(__byte_perm(mn, mx, 0x5410), __byte_perm(mn, mx, 0x7632));
 }
 
@@ -245,15 +260,17 @@ __device__ __forceinline__ Levels levels(uint32_t both) {
     v.s = 0.f;
     v.pair &= 0xffff0000u;
   }
-  v.r = v.s > 0.f ? __frcp_rn(v.s) : 0.f;
+  v.r = v.s > 0.f ? rcp_approx(v.s) : 0.f;
   return v;
 }
 
 // The codes of a chunk, value i in nibble i.  Many 16-bit values lie exactly between
-// two levels, so the quotient (x - min) / scale has to be the correctly rounded one:
-// x times the reciprocal, then one correction by its exact remainder (Markstein).  The
-// nearest integer is in the low bits of its sum with 1.5 * 2^23.
-template <bool BF16>
+// two levels, so where (x - min) / scale is a number with a half it has to come out
+// exactly: x times the reciprocal, then one correction by its exact remainder
+// (Markstein's), which leaves less than 2^-44 of an error before the last rounding.  The
+// nearest integer is in the low bits of the quotient's sum with 1.5 * 2^23.  CLAMP: a
+// subnormal fp16 scale may be far below (max - min) / 15.
+template <bool BF16, bool CLAMP>
 __device__ __forceinline__ uint32_t quantise(const Chunk& x, const Levels& v) {
   const uint64_t r2 = pack2(v.r, v.r), s2 = pack2(-v.s, -v.s), m2 = pack2(-v.low, -v.low);
   const uint64_t magic = pack2(12582912.f, 12582912.f);
@@ -263,7 +280,7 @@ __device__ __forceinline__ uint32_t quantise(const Chunk& x, const Levels& v) {
     const uint64_t a = add2(widen2<BF16>(x.w[i]), m2);
     uint64_t y = mul2(a, r2);
     y = fma2(fma2(s2, y, a), r2, y);
-    if (!BF16 && v.s < 0x1p-14f) {  // a subnormal scale may be far too small
+    if (CLAMP) {
       const float2 f = unpack2(y);
       y = pack2(fminf(f.x, 15.f), fminf(f.y, 15.f));
     }
@@ -278,32 +295,40 @@ __device__ __forceinline__ uint32_t quantise(const Chunk& x, const Levels& v) {
 // four or eight lanes of a group take part.  pair[1] is the second chunk's.
 template <bool BF16>
 __device__ __forceinline__ void quantise_row(const Chunk (&x)[2], int group, uint32_t (&codes)[2], uint32_t (&pair)[2]) {
-  uint32_t e0 = extremes<BF16>(x[0]), e1 = extremes<BF16>(x[1]);
+  Levels v0, v1;
   if (group == 32) {
+    uint32_t e0 = extremes<BF16>(x, 1), e1 = extremes<BF16>(x + 1, 1);
 #pragma unroll
     for (int s = 1; s < 4; s *= 2) {
       e0 = min2<BF16>(e0, __shfl_xor_sync(0xffffffffu, e0, s));
       e1 = min2<BF16>(e1, __shfl_xor_sync(0xffffffffu, e1, s));
     }
-    const Levels v0 = levels<BF16>(e0), v1 = levels<BF16>(e1);
-    codes[0] = quantise<BF16>(x[0], v0);
-    codes[1] = quantise<BF16>(x[1], v1);
-    pair[0] = v0.pair;
-    pair[1] = v1.pair;
+    v0 = levels<BF16>(e0);
+    v1 = levels<BF16>(e1);
   } else {
-    e0 = min2<BF16>(e0, e1);
-    for (int s = 1; s < group / 16; s *= 2) e0 = min2<BF16>(e0, __shfl_xor_sync(0xffffffffu, e0, s));
-    const Levels v = levels<BF16>(e0);
-    codes[0] = quantise<BF16>(x[0], v);
-    codes[1] = quantise<BF16>(x[1], v);
-    pair[0] = pair[1] = v.pair;
+    uint32_t e = extremes<BF16>(x, 2);
+    for (int s = 1; s < group / 16; s *= 2) e = min2<BF16>(e, __shfl_xor_sync(0xffffffffu, e, s));
+    v0 = v1 = levels<BF16>(e);
   }
+  if (!BF16 && __any_sync(0xffffffffu, fminf(v0.s, v1.s) < 0x1p-14f)) {
+    codes[0] = quantise<BF16, true>(x[0], v0);
+    codes[1] = quantise<BF16, true>(x[1], v1);
+  } else {
+    codes[0] = quantise<BF16, false>(x[0], v0);
+    codes[1] = quantise<BF16, false>(x[1], v1);
+  }
+  pair[0] = v0.pair;
+  pair[1] = v1.pair;
 }
 
+// Two rows in flight a lane and 28 to 32 warps an SM: four rows and 20 warps measured 63
+// against 65 us (16-bit, four prompts of 4096, 6.3 TB/s of traffic) but 30 against 28 us
+// for uneven chunks at d = 256; 4-bit: 60 us (5.9 TB/s) against 62.  A queue of single
+// rows ahead of the one at work was slower (69 to 80 us): loads and stores alternate then.
 template <int D, bool BF16, bool INT4>
-__global__ void __launch_bounds__(kThreads, INT4 ? 5 : 6) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
+__global__ void __launch_bounds__(kThreads, INT4 ? 7 : 8) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
   constexpr int LPT = D / 16, TPW = 32 / LPT;  // lanes of a token, tokens of a warp
-  constexpr int U = 4;                         // rows in flight
+  constexpr int U = 2;                         // rows in flight
   check_prefix(p.cu, p.b, p.total, p.status);
   const int lane = threadIdx.x & 31, k = lane % LPT;
   const unsigned w = (blockIdx.x * kThreads + threadIdx.x) >> 5;
@@ -492,10 +517,11 @@ __global__ void __launch_bounds__(kThreads, INT4 ? 5 : 6) kv_append_kernel(const
   }
 }
 
+// One head of a token at a time (two or four in flight measured no faster: 18 to 23 us
+// for four sequences of 4096 keys of eight heads, d = 128, at 48 warps an SM).
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads) kv_gather4_kernel(const __grid_constant__ KvGatherParams p) {
+__global__ void __launch_bounds__(kThreads, 12) kv_gather4_kernel(const __grid_constant__ KvGatherParams p) {
   constexpr int LPT = D / 16, TPW = 32 / LPT;
-  constexpr int U = 4;
   check_prefix(p.cu, p.b, p.total, p.status);
   const int lane = threadIdx.x & 31, k = lane % LPT;
   const unsigned w = (blockIdx.x * kThreads + threadIdx.x) >> 5;
@@ -511,62 +537,46 @@ __global__ void __launch_bounds__(kThreads) kv_gather4_kernel(const __grid_const
   const uint32_t mine = r % 2 != 0 ? 0x7632u : 0x5410u;  // the key's half of two words of V
   uint16_t* to[2] = {static_cast<uint16_t*>(p.k) + tok * p.k_st[0] + 8 * chunk,
                      static_cast<uint16_t*>(p.v) + tok * p.v_st[0] + 8 * chunk};
-  for (int h0 = part; h0 < p.hkv; h0 += U * parts) {
-    uint2 kw[U], v0[U], v1[U];
-    uint32_t pair[U][2][2];
+  for (int h = part; h < p.hkv; h += parts) {
+    const uint8_t* unit = base + h * p.c_st[1];
+    const uint32_t* vw = reinterpret_cast<const uint32_t*>(unit + 16 * D);
+    const uint32_t* par = reinterpret_cast<const uint32_t*>(unit + 32 * D) + r * ng;
+    const uint2 kw = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint32_t*>(unit) + kv4_k_word(D, r, chunk));
+    const uint2 v0 = *reinterpret_cast<const uint2*>(vw + kv4_v_half(D, r, 2 * chunk) / 2);
+    const uint2 v1 = *reinterpret_cast<const uint2*>(vw + kv4_v_half(D, r, 2 * chunk + 1) / 2);
+    const uint32_t pair[2][2] = {{par[g0], par[g1]}, {par[32 * ng + g0], par[32 * ng + g1]}};
+    const uint32_t codes[2][2] = {{kw.x, kw.y}, {__byte_perm(v0.x, v1.x, mine), __byte_perm(v0.y, v1.y, mine)}};
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * parts;
-      if (h >= p.hkv) break;
-      const uint8_t* unit = base + h * p.c_st[1];
-      const uint32_t* vw = reinterpret_cast<const uint32_t*>(unit + 16 * D);
-      const uint32_t* par = reinterpret_cast<const uint32_t*>(unit + 32 * D) + r * ng;
-      kw[u] = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint32_t*>(unit) + kv4_k_word(D, r, chunk));
-      v0[u] = *reinterpret_cast<const uint2*>(vw + kv4_v_half(D, r, 2 * chunk) / 2);
-      v1[u] = *reinterpret_cast<const uint2*>(vw + kv4_v_half(D, r, 2 * chunk + 1) / 2);
+    for (int kv = 0; kv < 2; ++kv) {
+      uint16_t* dst = to[kv] + h * (kv == 0 ? p.k_st[1] : p.v_st[1]);
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        pair[u][kv][0] = par[kv * 32 * ng + g0];
-        pair[u][kv][1] = g1 == g0 ? pair[u][kv][0] : par[kv * 32 * ng + g1];
-      }
-    }
+      for (int c = 0; c < 2; ++c) {
+        const float sc = widen1<BF16>(pair[kv][c] & 0xffffu), mn = widen1<BF16>(pair[kv][c] >> 16);
+        const uint64_t s2 = pack2(sc, sc), m2 = pack2(mn, mn), off = pack2(-1024.f, -1024.f);
+        // nibbles i and i + 4 of a word as the fp16 pair 1024 + code, then fp32; scale * code
+        // is exact, so the fused sum is min + scale * code rounded once
+        float f[8];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * parts;
-      if (h >= p.hkv) break;
-      const uint32_t codes[2][2] = {{kw[u].x, kw[u].y},
-                                    {__byte_perm(v0[u].x, v1[u].x, mine), __byte_perm(v0[u].y, v1[u].y, mine)}};
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        uint16_t* dst = to[kv] + h * (kv == 0 ? p.k_st[1] : p.v_st[1]);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float sc = widen1<BF16>(pair[u][kv][c] & 0xffffu), mn = widen1<BF16>(pair[u][kv][c] >> 16);
-          const uint64_t s2 = pack2(sc, sc), m2 = pack2(mn, mn), off = pack2(-1024.f, -1024.f);
-          // nibbles i and i + 4 of a word as the fp16 pair 1024 + code, then fp32; scale * code
-          // is exact, so the fused sum is min + scale * code rounded once
-          float f[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t two = ((codes[kv][c] >> (4 * i)) & 0x000f000fu) | 0x64006400u;
-            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&two));
-            const float2 y = unpack2(fma2(s2, add2(pack2(x.x, x.y), off), m2));
-            f[i] = y.x;
-            f[i + 4] = y.y;
-          }
-          store_chunk(dst + 32 * c, Chunk{{narrow2<BF16>(f[0], f[1]), narrow2<BF16>(f[2], f[3]), narrow2<BF16>(f[4], f[5]),
-                                           narrow2<BF16>(f[6], f[7])}});
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t two = ((codes[kv][c] >> (4 * i)) & 0x000f000fu) | 0x64006400u;
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&two));
+          const float2 y = unpack2(fma2(s2, add2(pack2(x.x, x.y), off), m2));
+          f[i] = y.x;
+          f[i + 4] = y.y;
         }
+        store_chunk(dst + 32 * c, Chunk{{narrow2<BF16>(f[0], f[1]), narrow2<BF16>(f[2], f[3]), narrow2<BF16>(f[4], f[5]),
+                                         narrow2<BF16>(f[6], f[7])}});
       }
     }
   }
 }
 
-// Warps that share a token's rows, and the blocks of the launch: as many warps as keep
-// every SM busy (32 each), at least two rows a warp where there are that many tokens.
-unsigned deal(int64_t total, int rows, int d, int sms, int* parts) {
+// Warps that share a token's rows, and the blocks of the launch: `warps` of them where
+// there are rows enough.  (Appending four prompts of 4096 tokens, 32 / 8 heads of 128:
+// 16 warps an SM measured 73 us, 32 65 us, 64 64 us, but 64 cost the 4-bit append 6%.)
+unsigned deal(int64_t total, int rows, int d, int warps, int* parts) {
   const int64_t groups = (total * (d / 16) + 31) / 32;  // warps that hold the tokens once
-  int64_t n = (static_cast<int64_t>(sms) * 32 + groups - 1) / groups;
+  int64_t n = (static_cast<int64_t>(warps) + groups - 1) / groups;
   if (n > rows) n = rows;
   if (n < 1) n = 1;
   *parts = static_cast<int>(n);
@@ -588,7 +598,7 @@ void launch_append_d(const KvAppendParams& p, int dtype, unsigned grid, cudaStre
 }  // namespace
 
 cudaError_t launch_kv_append(KvAppendParams& p, int dtype, int sms, cudaStream_t stream) {
-  const unsigned grid = deal(p.total, p.hq + 2 * p.hkv, p.d, sms, &p.parts);
+  const unsigned grid = deal(p.total, p.hq + 2 * p.hkv, p.d, 32 * sms, &p.parts);
   if (p.d == 64) launch_append_d<64>(p, dtype, grid, stream);
   else if (p.d == 128) launch_append_d<128>(p, dtype, grid, stream);
   else launch_append_d<256>(p, dtype, grid, stream);
@@ -596,7 +606,7 @@ cudaError_t launch_kv_append(KvAppendParams& p, int dtype, int sms, cudaStream_t
 }
 
 cudaError_t launch_kv_gather4(KvGatherParams& p, int dtype, int sms, cudaStream_t stream) {
-  const unsigned grid = deal(p.total, p.hkv, p.d, sms, &p.parts);
+  const unsigned grid = deal(p.total, p.hkv, p.d, 64 * sms, &p.parts);
   if (dtype == 0) {
     if (p.d == 64) kv_gather4_kernel<64, true><<<grid, kThreads, 0, stream>>>(p);
     else if (p.d == 128) kv_gather4_kernel<128, true><<<grid, kThreads, 0, stream>>>(p);
