@@ -47,6 +47,25 @@ def test_struct_layouts(tmp_path):
             assert (f.offset, f.size) == (int(a), int(b)), (struct, name)
 
 
+def test_packers_match_the_mirrors():
+    """The packers put every value where the ctypes mirrors (checked against the header) have it."""
+    import ctypes as ct
+
+    from tiled_exact_attention_gb300 import _lib
+
+    for packer, mirror in ((_lib.KV_APPEND, _lib.KvAppendArgs), (_lib.KV_GATHER_INT4, _lib.KvGatherInt4Args),
+                           (_lib.KVCACHE_INT4, _lib.KvcacheInt4Args)):
+        flat = sum(getattr(t, "_length_", 1) for _, t in mirror._fields_)
+        raw = packer.pack(*range(1, flat + 1))
+        assert len(raw) == ct.sizeof(mirror)
+        got, n = mirror.from_buffer_copy(raw), 0
+        for name, t in mirror._fields_:
+            value = getattr(got, name)
+            for x in (list(value) if hasattr(t, "_length_") else [value]):
+                n += 1
+                assert x == n, (mirror.__name__, name)
+
+
 def _append_args(**kw):
     from tiled_exact_attention_gb300._lib import KvAppendArgs
 

@@ -13,8 +13,8 @@ import math
 import torch
 
 from . import _lib
-from ._lib import (FA_BF16, FA_FP16, FA_OFFSET_BOTTOM_RIGHT, BwdArgs, E4m3Args, FwdArgs, KvAppendArgs, KvcacheArgs,
-                   KvcacheInt4Args, KvGatherInt4Args, QuantArgs, SplitkvE4m3Args, VarlenArgs, check)
+from ._lib import (FA_BF16, FA_FP16, FA_OFFSET_BOTTOM_RIGHT, KV_APPEND, KV_GATHER_INT4, KVCACHE_INT4, BwdArgs,
+                   E4m3Args, FwdArgs, KvcacheArgs, QuantArgs, SplitkvE4m3Args, VarlenArgs, check)
 
 _DT = {torch.bfloat16: FA_BF16, torch.float16: FA_FP16}
 
@@ -458,16 +458,20 @@ def fa_fwd_splitkv_e4m3(q, k8, k_descale, v8, v_descale, *, scale=None, num_spli
     return out, lse
 
 
-def _enqueue(fn, args, device: int, stream, *more):
+# What the paged cache's entry points share.  They are called once per layer and token, so their arguments are looked
+# over and packed in one pass.
+
+_NOT_ROWS = "every row tensor must be a CUDA tensor of one type (bf16 or fp16), on one device, contiguous in its last " \
+    "dimension, and shaped like its counterpart"
+
+
+def _enqueue(fn, args: bytes, device: int, stream, *more):
     """fn(args, *more, stream) with the tensors' device current (kernels launch on the current device)."""
-    if stream is not None:
-        raw = stream.cuda_stream
-    else:
-        raw = torch._C._cuda_getCurrentRawStream(device)
+    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
     if device == torch.cuda.current_device():
-        return fn(ctypes.byref(args), *more, raw)
+        return fn(args, *more, raw)
     with torch.cuda.device(device):
-        return fn(ctypes.byref(args), *more, raw)
+        return fn(args, *more, raw)
 
 
 def _new(stream, device, shape, dtype):
@@ -478,20 +482,26 @@ def _new(stream, device, shape, dtype):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _dense_strides(t: torch.Tensor, shape):
-    """Strides of all but the last dimension; those of dimensions of one entry are never used and get a valid value."""
-    st = t.stride()
-    if st[-1] != 1:
-        raise ValueError("every tensor must be contiguous in its last dimension")
-    if 1 in shape[:-1]:
-        return tuple(shape[-1] if n == 1 else x for n, x in zip(shape[:-1], st))
-    return st[:-1]
+def _rows3(t, device: int, dtype, n: int, h: int, d: int):
+    """(pointer, row stride, head stride) of a [n, h, d] tensor; the stride of a dimension of one entry is never used
+    and gets a valid value."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device or t.shape != (n, h, d):
+        raise ValueError(_NOT_ROWS)
+    row, head, last = t.stride()
+    if last != 1:
+        raise ValueError(_NOT_ROWS)
+    return t.data_ptr(), row if n > 1 else d, head if h > 1 else d
 
 
-def _check_rows(device: int, dtype, *named):
-    for name, t in named:
-        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device:
-            raise ValueError(f"{name} must be a CUDA tensor of the type of the others, on their device")
+def _rows4(t, device: int, dtype, shape):
+    """(pointer, three strides) of a 4-D tensor, likewise."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device or t.shape != shape:
+        raise ValueError(_NOT_ROWS)
+    s0, s1, s2, last = t.stride()
+    if last != 1:
+        raise ValueError(_NOT_ROWS)
+    n0, n1, n2, d = shape
+    return t.data_ptr(), s0 if n0 > 1 else d, s1 if n1 > 1 else d, s2 if n2 > 1 else d
 
 
 def _pages(device: int, block_table, seqlens_k):
@@ -511,12 +521,12 @@ def _pages(device: int, block_table, seqlens_k):
     return b, block_table.data_ptr(), row if b > 1 else width, seqlens_k.data_ptr()
 
 
-def _prefix(device: int, cu_seqlens, b: int, total: int):
-    """Pointer of the prefix sums, None where every sequence has the same number of rows."""
+def _prefix(device: int, cu_seqlens, b: int, total: int) -> int:
+    """Pointer of the prefix sums, 0 where every sequence has the same number of rows."""
     if cu_seqlens is None:
         if b == 0 or total % b:
             raise ValueError("without cu_seqlens every sequence has the same number of rows")
-        return None
+        return 0
     if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dtype is not torch.int32 \
             or cu_seqlens.get_device() != device or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] != b + 1 \
             or cu_seqlens.stride(0) != 1:
@@ -526,8 +536,8 @@ def _prefix(device: int, cu_seqlens, b: int, total: int):
 
 
 def _cache4(device: int, cache, group: int, d: int, hkv):
-    """(pointer, (page, head) strides, pages, page size, KV heads) of a 4-bit cache; the page size follows from the
-    bytes of a page."""
+    """(pointer, page stride, head stride, pages, page size, KV heads) of a 4-bit cache; the page size follows from
+    the bytes of a page."""
     if not isinstance(cache, torch.Tensor) or cache.dtype is not torch.uint8 or cache.get_device() != device \
             or cache.dim() != 3:
         raise ValueError("cache must be a CUDA uint8 [num_pages, hkv, page bytes] tensor on the device of the others")
@@ -542,38 +552,32 @@ def _cache4(device: int, cache, group: int, d: int, hkv):
     sp, sh, last = cache.stride()
     if last != 1:
         raise ValueError("cache must be contiguous in its last dimension")
-    return (cache.data_ptr(), (sp if pages > 1 else size * heads, sh if heads > 1 else size), pages, size // per_key,
+    return (cache.data_ptr(), sp if pages > 1 else size * heads, sh if heads > 1 else size, pages, size // per_key,
             heads)
 
 
-_NO2, _NO3 = (0, 0), (0, 0, 0)
-
-
-def _make_append_args(device: int, k, v, block_table, seqlens_k, cu_seqlens, q, q_out, cos_sin, rotary_dim, interleaved,
-                      k_cache=None, v_cache=None, cache=None, group=0) -> KvAppendArgs:
+def _append_args(device: int, k, v, block_table, seqlens_k, cu_seqlens, q, q_out, cos_sin, rotary_dim, interleaved,
+                 k_cache, v_cache, cache, group) -> bytes:
     """`fa_kv_append_args` of either cache.  q, q_out: [total, hq, d]; k, v: [total, hkv, d]; cos_sin: fp32
     [max_positions, rotary_dim], cosines then sines."""
     dtype = k.dtype
-    if device < 0 or dtype not in _DT:
-        raise ValueError("k must be a CUDA bf16 or fp16 tensor")
-    _check_rows(device, dtype, ("v", v))
-    shape = k.shape
-    if len(shape) != 3 or v.shape != shape:
-        raise ValueError("k and v must both be [total, hkv, d]")
-    total, hkv, d = shape
+    if device < 0 or dtype not in _DT or k.dim() != 3:
+        raise ValueError("k must be a CUDA bf16 or fp16 [total, hkv, d] tensor")
+    total, hkv, d = k.shape
+    k_at, k0, k1 = _rows3(k, device, dtype, total, hkv, d)
+    v_at, v0, v1 = _rows3(v, device, dtype, total, hkv, d)
     b, table, row, lens = _pages(device, block_table, seqlens_k)
     cu = _prefix(device, cu_seqlens, b, total)
-    hq, q_at, qo_at, q_st, qo_st = 0, None, None, _NO2, _NO2
+    hq = q_at = q0 = q1 = qo_at = qo0 = qo1 = 0
     if q is not None:
-        _check_rows(device, dtype, ("q", q), ("q_out", q_out))
-        qs = q.shape
-        if len(qs) != 3 or qs[0] != total or qs[2] != d or q_out.shape != qs:
-            raise ValueError("q and q_out must both be [total, hq, d]")
-        hq, q_at, qo_at = qs[1], q.data_ptr(), q_out.data_ptr()
-        q_st, qo_st = _dense_strides(q, qs), _dense_strides(q_out, qs)
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be [total, hq, d]")
+        hq = q.shape[1]
+        q_at, q0, q1 = _rows3(q, device, dtype, total, hq, d)
+        qo_at, qo0, qo1 = _rows3(q_out, device, dtype, total, hq, d)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    cs_at, rot, positions = None, 0, 0
+    cs_at = rot = positions = 0
     if cos_sin is not None:
         if not isinstance(cos_sin, torch.Tensor) or cos_sin.dtype is not torch.float32 \
                 or cos_sin.get_device() != device or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
@@ -584,21 +588,20 @@ def _make_append_args(device: int, k, v, block_table, seqlens_k, cu_seqlens, q, 
             raise ValueError("rotary_dim must be the width of cos_sin")
     elif rotary_dim:
         raise ValueError("a rotation needs cos_sin")
-    kc_at, vc_at, kc_st, vc_st, c_at, c_st = None, None, _NO3, _NO3, None, _NO2
     if cache is None:
-        _check_rows(device, dtype, ("k_cache", k_cache), ("v_cache", v_cache))
-        cs = k_cache.shape
-        if len(cs) != 4 or v_cache.shape != cs or cs[2] != hkv or cs[3] != d:
+        shape = k_cache.shape
+        if len(shape) != 4 or shape[2] != hkv or shape[3] != d:
             raise ValueError("k_cache and v_cache must both be [num_pages, page_size, hkv, d]")
-        pages, page_size = cs[0], cs[1]
-        kc_at, vc_at = k_cache.data_ptr(), v_cache.data_ptr()
-        kc_st, vc_st = _dense_strides(k_cache, cs), _dense_strides(v_cache, cs)
-    else:
-        c_at, c_st, pages, page_size, _ = _cache4(device, cache, group, d, hkv)
-    return KvAppendArgs(_DT[dtype], b, total, hq, hkv, d, q_at, qo_at, k.data_ptr(), v.data_ptr(), q_st, qo_st,
-                        _dense_strides(k, shape), _dense_strides(v, shape), cu, lens, cs_at, rot, positions,
-                        1 if interleaved else 0, pages, page_size, table, row, kc_at, vc_at, kc_st, vc_st, c_at, c_st,
-                        group)
+        pages, page_size = shape[0], shape[1]
+        kc, kc0, kc1, kc2 = _rows4(k_cache, device, dtype, shape)
+        vc, vc0, vc1, vc2 = _rows4(v_cache, device, dtype, shape)
+        return KV_APPEND.pack(_DT[dtype], b, total, hq, hkv, d, q_at, qo_at, k_at, v_at, q0, q1, qo0, qo1, k0, k1, v0,
+                              v1, cu, lens, cs_at, rot, positions, 1 if interleaved else 0, pages, page_size, table,
+                              row, kc, vc, kc0, kc1, kc2, vc0, vc1, vc2, 0, 0, 0, 0)
+    c, c0, c1, pages, page_size, _ = _cache4(device, cache, group, d, hkv)
+    return KV_APPEND.pack(_DT[dtype], b, total, hq, hkv, d, q_at, qo_at, k_at, v_at, q0, q1, qo0, qo1, k0, k1, v0, v1,
+                          cu, lens, cs_at, rot, positions, 1 if interleaved else 0, pages, page_size, table, row, 0, 0,
+                          0, 0, 0, 0, 0, 0, c, c0, c1, group)
 
 
 def fa_kv_append(k, v, k_cache, v_cache, *, block_table, seqlens_k, cu_seqlens=None, q=None, q_out=None, cos_sin=None,
@@ -609,8 +612,10 @@ def fa_kv_append(k, v, k_cache, v_cache, *, block_table, seqlens_k, cu_seqlens=N
     device = k.get_device()
     if q is not None and q_out is None and device >= 0:
         q_out = _new(stream, k.device, q.shape, q.dtype)
-    a = _make_append_args(device, k, v, block_table, seqlens_k, cu_seqlens, q, q_out, cos_sin, rotary_dim, interleaved,
-                          k_cache, v_cache)
+    if not isinstance(k_cache, torch.Tensor) or not isinstance(v_cache, torch.Tensor):
+        raise ValueError("k_cache and v_cache must both be [num_pages, page_size, hkv, d]")
+    a = _append_args(device, k, v, block_table, seqlens_k, cu_seqlens, q, q_out, cos_sin, rotary_dim, interleaved,
+                     k_cache, v_cache, None, 0)
     check(_enqueue(_lib.load().fa_kv_append, a, device, stream), "fa_kv_append")
     return q_out
 
@@ -624,8 +629,8 @@ def fa_kv_append_int4(k, v, cache, *, group: int, block_table, seqlens_k, cu_seq
         raise ValueError("a 4-bit cache is needed")
     if q is not None and q_out is None and device >= 0:
         q_out = _new(stream, k.device, q.shape, q.dtype)
-    a = _make_append_args(device, k, v, block_table, seqlens_k, cu_seqlens, q, q_out, cos_sin, rotary_dim, interleaved,
-                          cache=cache, group=group)
+    a = _append_args(device, k, v, block_table, seqlens_k, cu_seqlens, q, q_out, cos_sin, rotary_dim, interleaved,
+                     None, None, cache, group)
     check(_enqueue(_lib.load().fa_kv_append_int4, a, device, stream), "fa_kv_append_int4")
     return q_out
 
@@ -650,16 +655,17 @@ def fa_kv_gather_int4(cache, *, group: int, block_table, seqlens_k, cu_seqlens=N
             raise ValueError("total, d and dtype are needed to allocate the rows")
         shape = (int(total), cache.shape[1], int(d))
         k_out, v_out = _new(stream, cache.device, shape, dtype), _new(stream, cache.device, shape, dtype)
-    dtype, shape = k_out.dtype, k_out.shape
-    _check_rows(device, dtype, ("k_out", k_out), ("v_out", v_out))
-    if dtype not in _DT or len(shape) != 3 or v_out.shape != shape:
+    dtype = k_out.dtype
+    if dtype not in _DT or k_out.dim() != 3:
         raise ValueError("k_out and v_out must both be bf16 or fp16 [total, hkv, d]")
-    total, hkv, d = shape
+    total, hkv, d = k_out.shape
+    k_at, k0, k1 = _rows3(k_out, device, dtype, total, hkv, d)
+    v_at, v0, v1 = _rows3(v_out, device, dtype, total, hkv, d)
     b, table, row, lens = _pages(device, block_table, seqlens_k)
     cu = _prefix(device, cu_seqlens, b, total)
-    c_at, c_st, pages, page_size, _ = _cache4(device, cache, group, d, hkv)
-    a = KvGatherInt4Args(_DT[dtype], b, total, hkv, d, group, c_at, c_st, pages, page_size, table, row, lens, cu,
-                         k_out.data_ptr(), v_out.data_ptr(), _dense_strides(k_out, shape), _dense_strides(v_out, shape))
+    c, c0, c1, pages, page_size, _ = _cache4(device, cache, group, d, hkv)
+    a = KV_GATHER_INT4.pack(_DT[dtype], b, total, hkv, d, group, c, c0, c1, pages, page_size, table, row, lens, cu,
+                            k_at, v_at, k0, k1, v0, v1)
     check(_enqueue(_lib.load().fa_kv_gather_int4, a, device, stream), "fa_kv_gather_int4")
     return k_out, v_out
 
@@ -675,32 +681,32 @@ def fa_fwd_kvcache_int4(q, cache, *, group: int, block_table, seqlens_k, scale=N
         b, sq, hq, d = shape
         lse_shape = (b, hq, sq)
     else:
-        b, hq, d = lse_shape = shape
+        b, hq, d = shape
         sq, lse_shape = 1, (b, hq)
     if out is None:
         out = _new(stream, q.device, shape, dtype)
-    else:
-        _check_rows(device, dtype, ("out", out))
-        if out.shape != shape:
-            raise ValueError("out must be shaped like q")
     if lse is None:
         lse = _new(stream, q.device, lse_shape, torch.float32)
     elif lse.shape != lse_shape or lse.dtype is not torch.float32 or lse.get_device() != device \
             or not lse.is_contiguous():
         raise ValueError("lse must be contiguous CUDA fp32 [b, hq, sq] (or [b, hq])")
+    if len(shape) == 4:
+        q_at, q0, q1, q2 = _rows4(q, device, dtype, shape)
+        o_at, o0, o1, o2 = _rows4(out, device, dtype, shape)
+    else:
+        q_at, q0, q2 = _rows3(q, device, dtype, b, hq, d)
+        o_at, o0, o2 = _rows3(out, device, dtype, b, hq, d)
+        q1 = o1 = d
     seqs, table, row, lens = _pages(device, block_table, seqlens_k)
     if seqs != b:
         raise ValueError("block_table must be [b, n] and seqlens_k [b]")
-    c_at, c_st, pages, page_size, hkv = _cache4(device, cache, group, d, None)
-    q_st, o_st = _dense_strides(q, shape), _dense_strides(out, shape)
-    if len(shape) == 3:
-        q_st, o_st = (q_st[0], d, q_st[1]), (o_st[0], d, o_st[1])
-    a = KvcacheInt4Args(_DT[dtype], b, sq, hq, hkv, d, group, q.data_ptr(), q_st, c_at, c_st, pages, page_size, table,
-                        row, lens, out.data_ptr(), o_st, lse.data_ptr(), d ** -0.5 if scale is None else scale,
-                        0 if window_left is None else 1, 0 if window_left is None else window_left, softcap)
+    c, c0, c1, pages, page_size, hkv = _cache4(device, cache, group, d, None)
+    a = KVCACHE_INT4.pack(_DT[dtype], b, sq, hq, hkv, d, group, q_at, q0, q1, q2, c, c0, c1, pages, page_size, table,
+                          row, lens, o_at, o0, o1, o2, lse.data_ptr(), d ** -0.5 if scale is None else scale,
+                          0 if window_left is None else 1, 0 if window_left is None else window_left, softcap)
     lib = _lib.load()
     if workspace is None:
-        need = _enqueue(lambda args, s: lib.fa_kvcache_int4_workspace_size(args), a, device, stream)
+        need = _enqueue(lambda args, _: lib.fa_kvcache_int4_workspace_size(args), a, device, stream)
         workspace = _new(stream, q.device, (max(int(need), 256),), torch.uint8)
     elif workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
