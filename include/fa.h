@@ -549,8 +549,8 @@ fa_status fa_kv_gather_int4(const fa_kv_gather_int4_args* args, void* stream);
  * sees keys j <= t, with local = 1 only those j >= t - window_left; a query that sees
  * no key (a negative position) gets O = 0, LSE = -inf.  Scores, softcap, softmax and
  * LSE as in fa_fwd_args, statistics in fp32.  Made for few queries (decode, drafted
- * tokens): every 16 rows (query tokens x query heads of a KV head) read the cache
- * once; a long chunk goes through fa_kv_gather_int4 and fa_fwd_varlen.  The cache
+ * tokens): every 16 rows (query tokens x query heads of a KV head; every 8 at d = 256)
+ * read the cache once; a long chunk goes through fa_kv_gather_int4 and fa_fwd_varlen.  The cache
  * beyond a sequence's length is never used, whatever it holds.  Lengths and pages are
  * checked on the device: a sequence longer than its block-table row, or a page
  * outside [0, num_pages), is not read, FA_ERR_DEVICE_ARG is recorded and that

@@ -8,9 +8,11 @@
 // five integer instructions, with no conversion.  The factor 2^-24 goes into the
 // score's scale, the factor 16 into Q (exactly: powers of two).  O is likewise
 //   sum_j (p_j s_vj) (c_j - 8) + sum_j p_j (min_vj + 8 s_vj),
-// the weights p s_v rounded to fp16 for the MMA and 8 times their sum as rounded taken
-// off in fp32, so the rounding multiplies only the centred part of V.  Scores, the
-// running maximum and sum, and O are fp32.
+// the weights p s_v rounded to fp16 for the MMA, so the rounding multiplies only the
+// centred part of V; the 8 is taken off in fp32 at the end.  (The ones that sum the
+// weights are the fp16 1.0: products of the subnormal 2^-24 lose their low bits in the
+// tensor core when larger ones stand beside them, which cost 3.3e-3 of O at 32768 keys.)
+// Scores, the running maximum and sum, and O are fp32.
 //
 // Layout of the work.  K (keys x dims) and V^T (dims x keys) are the A operands, 16
 // rows an MMA; the rows of queries (query tokens x the g query heads that share the
@@ -41,10 +43,13 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kGap = 12;            // what an item costs besides its blocks, in blocks
 constexpr int kMinShare = 4 + kGap;  // a CTA's stretch of the line at least ...
 constexpr int kUncut = 16;      // ... and items of up to so many blocks are never cut
-constexpr int kMostParts = 64;  // CTAs that share an item at most
+constexpr int kMostParts = 32;  // CTAs that share an item at most
 constexpr float kLn2 = 0.69314718055994530942f;
 
 enum : int { kSiteFull = 48 };
+
+// fp16 pairs of -8 2^-24 and -128 2^-24: what takes 8 off a code, in its row's factor.
+constexpr uint32_t kLess8 = 0x80088008u, kLess128 = 0x80808080u;
 
 template <int D, int NG, int NT>
 struct Cfg {
@@ -57,10 +62,16 @@ struct Cfg {
   static constexpr int DP = D < 128 ? D : 128;  // dims of O that the warps exchange at a time
   static constexpr int OP = DP + 4;             // pitch of a row there (floats)
   static constexpr int RING = kWarps * STAGES * STAGE;
-  static constexpr int SMEM = RING + kWarps * ROWS * OP * 4 + kWarps * ROWS * 8 + kWarps * STAGES * 8 + 16;
-  static constexpr int CTAS = NT == 1 && SMEM <= 74 * 1024 ? 3 : (SMEM <= 112 * 1024 ? 2 : 1);  // per SM
-  static constexpr bool ONES = NG <= 2 || (NG == 4 && NT == 1);
-  static_assert(kMostParts * ROWS * 4 <= kWarps * ROWS * OP * 4, "the merge's weights fit the exchange buffer");
+  static constexpr int SMEM = RING + kMostParts * ROWS * 4 + kWarps * ROWS * 8 + kWarps * STAGES * 8 + kWarps * 4 + 16;
+  static constexpr int FIT = 227 * 1024 / (SMEM + 1024);
+  static constexpr int WANT = NT == 1 && D == 64 ? 3 : 2;
+  static constexpr int CTAS = FIT < WANT ? FIT : WANT;  // per SM
+  // How 8 is taken off the codes of V: by the sum of the weights from one more MMA a
+  // group, with ones, where there are registers for it, else by a second MMA per word
+  // with a constant A (8 x 32768 keys, d = 128: 56.4 against 61.0 us; 6 windows of 4096
+  // keys, d = 256: 19.4 against 20.1).
+  static constexpr bool ONES = NG * NT <= 4;
+  static_assert(ROWS * OP * 4 <= STAGE, "a warp's share of O fits the stage that it read last");
 };
 
 template <bool BF16>
@@ -80,22 +91,28 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&x);
 }
 
+// c += a b, or c = a b where `first` (a constant).
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                                         uint32_t b0, uint32_t b1, bool first = false) {
+  if (first) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  } else {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
 }
 
-// The same into a fresh accumulator.
-__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                               uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %10, %10, %10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+// (x, y) += a + b, in packed fp32.
+__device__ __forceinline__ void add_pair(float& x, float& y, const float* a, const float* b) {
+  asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 w, {%4, %5};\n\t"
+      "add.rn.f32x2 v, v, w;\n\tadd.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -239,11 +256,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * C::STAGES * C::STAGE;
-  float* obuf = reinterpret_cast<float*>(smem + C::RING);               // [kWarps][ROWS][OP]
-  float2* ml = reinterpret_cast<float2*>(obuf + kWarps * ROWS * C::OP);  // [kWarps][ROWS]
+  float* wbuf = reinterpret_cast<float*>(smem + C::RING);                // [kMostParts][ROWS]
+  float2* ml = reinterpret_cast<float2*>(wbuf + kMostParts * ROWS);      // [kWarps][ROWS]
   uint64_t* bars = reinterpret_cast<uint64_t*>(ml + kWarps * ROWS);
   uint64_t* full = bars + warp * C::STAGES;
-  int* last_in = reinterpret_cast<int*>(bars + kWarps * C::STAGES);
+  int* held = reinterpret_cast<int*>(bars + kWarps * C::STAGES);  // [kWarps]: the stage with the warp's share of O
+  int* last_in = held + kWarps;
 
   if (lane == 0) {
     for (int s = 0; s < C::STAGES; ++s) mbar_init(&full[s], 1);
@@ -434,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
           qs[q][nt][c] = __shfl_sync(0xffffffffu, sum[q], 4 * (2 * t + c));
           tv[q][nt][c] = 0.f;
         }
-        if (C::ONES) {
+        if constexpr (C::ONES) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) ones[q][nt][e] = 0.f;
         }
@@ -448,6 +466,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
     int all_hi = it.len - p.sq, all_lo = it.hi - 1 - p.window_left;
     if (p.sq > 1) all_hi += it.tile * ROWS / p.g;
     if (p.window_left < 0) all_lo = 0;
+    int hold = -1;
     float vscale = 0.f;  // V's weights are held times this power of two (0: not chosen yet)
 
     if (it.hi > it.lo)
@@ -477,12 +496,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
               const uint32_t ha = wa[j] >> 8, hb = wb[j] >> 8;
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                if (w % GW == 0)
-                  mma16816_first(acc[nt], wa[j] & 0x000f000fu, wb[j] & 0x000f000fu, ha & 0x000f000fu, hb & 0x000f000fu,
-                                 qf[w][0][nt][0], qf[w][0][nt][1]);
-                else
-                  mma16816(acc[nt], wa[j] & 0x000f000fu, wb[j] & 0x000f000fu, ha & 0x000f000fu, hb & 0x000f000fu,
-                           qf[w][0][nt][0], qf[w][0][nt][1]);
+                mma16816(acc[nt], wa[j] & 0x000f000fu, wb[j] & 0x000f000fu, ha & 0x000f000fu, hb & 0x000f000fu,
+                         qf[w][0][nt][0], qf[w][0][nt][1], w % GW == 0);
                 mma16816(acc[nt], wa[j] & 0x00f000f0u, wb[j] & 0x00f000f0u, ha & 0x00f000f0u, hb & 0x00f000f0u,
                          qf[w][1][nt][0], qf[w][1][nt][1]);
               }
@@ -549,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
 #pragma unroll
               for (int q = 0; q < NG; ++q) {
                 tv[q][nt][c] *= a;
-                if (C::ONES) ones[q][nt][c] *= a;
+                if constexpr (C::ONES) ones[q][nt][c] *= a;
               }
 #pragma unroll
               for (int j = 0; j < NW; ++j) {
@@ -583,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
             const float now = __uint_as_float((261u - (__float_as_uint(top) >> 23)) << 23);
             if (vscale > 0.f) {
               const float a = now / vscale;
-              if (C::ONES) {
+              if constexpr (C::ONES) {
 #pragma unroll
                 for (int q = 0; q < NG; ++q)
 #pragma unroll
@@ -605,7 +620,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
             vscale = now;
           }
         }
-        const float off8 = vscale > 0.f ? -8.f / vscale : 0.f;
         // ---- probabilities and O
 #pragma unroll
         for (int mt = 0; mt < 2 * C::UNITS; ++mt) {
@@ -642,17 +656,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
               const uint32_t hb = pack_f16(pr[nt][2] * vb, pr[nt][3] * vb);
               tv[q][nt][0] = fmaf(pr[nt][0], na, fmaf(pr[nt][2], nb, tv[q][nt][0]));
               tv[q][nt][1] = fmaf(pr[nt][1], na, fmaf(pr[nt][3], nb, tv[q][nt][1]));
-              if (!C::ONES) {
-                const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&ha));
-                const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&hb));
-                tv[q][nt][0] = fmaf(fa.x + fb.x, off8, tv[q][nt][0]);
-                tv[q][nt][1] = fmaf(fa.y + fb.y, off8, tv[q][nt][1]);
-              }
               bw[q][nt][0] = transpose8(ha);
               bw[q][nt][1] = transpose8(hb);
-              if (C::ONES)  // the sum of the weights as rounded, in units of 2^-24
-                mma16816(ones[q][nt], 0x00010001u, 0u, 0x00010001u, 0u, bw[q][nt][0], bw[q][nt][1]);
+              if constexpr (C::ONES) mma16816(ones[q][nt], 0x3c003c00u, 0u, 0x3c003c00u, 0u, bw[q][nt][0], bw[q][nt][1]);
             }
+          }
+          if constexpr (!C::ONES) {
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma16816(o[w][0][nt], kLess8, kLess128, kLess8, kLess128, bw[w / GW][nt][0], bw[w / GW][nt][1]);
+                mma16816(o[w][1][nt], kLess8, kLess128, kLess8, kLess128, bw[w / GW][nt][0], bw[w / GW][nt][1]);
+              }
           }
           const uint8_t* vu = unit + 16 * D;
 #pragma unroll
@@ -675,7 +691,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
           }
         }
         __syncwarp();  // every lane has read the stage
-        copy_next(slot);
+        if (u + kWarps < cw.ue) copy_next(slot);
+        else hold = slot;  // (the last stage read carries the warp's share of O first)
         if (++slot == C::STAGES) {
           slot = 0;
           phase ^= 1u;
@@ -700,6 +717,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
 #pragma unroll
           for (int q = 0; q < NG; ++q) tv[q][nt][c] += __shfl_xor_sync(0xffffffffu, tv[q][nt][c], x);
         }
+    if (lane == 0) held[warp] = hold;
     if (g == 0) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -720,6 +738,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
 #pragma unroll
     for (int ps = 0; ps < D / C::DP; ++ps) {
       if (ps > 0) __syncthreads();
+      if (hold >= 0) {
+        float* mine = reinterpret_cast<float*>(ring + hold * C::STAGE);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -728,11 +748,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
           for (int j = 0; j < C::DP / 32; ++j) {
             const int w = ps * (C::DP / 32) + j;
             float add = tv[w / GW][nt][c];
-            if (C::ONES) add = fmaf(ones[w / GW][nt][c], -8.f * unscale, add);
-            *reinterpret_cast<float4*>(obuf + (warp * ROWS + nt * 8 + 2 * t + c) * C::OP + 32 * j + 4 * g) =
+            if constexpr (C::ONES) add = fmaf(ones[w / GW][nt][c], -0x1p-21f * unscale, add);
+            *reinterpret_cast<float4*>(mine + (nt * 8 + 2 * t + c) * C::OP + 32 * j + 4 * g) =
                 make_float4(fmaf(o[w][0][nt][c], unscale, add), fmaf(o[w][0][nt][c + 2], unscale * 0.0625f, add),
                             fmaf(o[w][1][nt][c], unscale, add), fmaf(o[w][1][nt][c + 2], unscale * 0.0625f, add));
           }
+        fence_proxy_async_smem();  // (the stage's next copy comes after these stores)
+      }
       __syncthreads();
       for (int x = threadIdx.x; x < ROWS * PER; x += kThreads) {
         const int r = x / PER, e = x % PER, row = it.tile * ROWS + r;
@@ -747,8 +769,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
         for (int k = 0; k < 8; ++k) f[k] = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float a = y[w].x == -INFINITY ? 0.f : ex2_approx(y[w].x - M);
-          const float4* from = reinterpret_cast<const float4*>(obuf + (w * ROWS + r) * C::OP + 8 * e);
+          if (y[w].x == -INFINITY) continue;  // (a warp without a block has no share)
+          const float a = ex2_approx(y[w].x - M);
+          const float4* from = reinterpret_cast<const float4*>(smem + (w * C::STAGES + held[w]) * C::STAGE) + (r * C::OP) / 4 + 2 * e;
           const float4 u = from[0], v = from[1];
           L = fmaf(y[w].y, a, L);
           f[0] = fmaf(u.x, a, f[0]);
@@ -780,7 +803,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
       __syncthreads();
       if (*last_in) {
         constexpr int TPR = kThreads / ROWS;  // threads of a row for the weights
-        float* wbuf = obuf;                   // [parts][ROWS]
         const int parts = c1 - c0 + 1;
         {
           const int r = threadIdx.x / TPR, k = threadIdx.x % TPR, row = it.tile * ROWS + r;
@@ -829,7 +851,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
         }
       }
     }
-    if (live) __syncthreads();  // the buffers are free again
+    if (live) {
+      __syncthreads();  // the buffers are free again
+      if (hold >= 0) copy_next(hold);
+    }
   }
 }
 
@@ -879,11 +904,16 @@ cudaError_t launch_dtype(const Attend4Params& p, int dtype, int sms, Attend4Plan
   return dtype == 0 ? launch_one<D, NG, true, NT>(p, p.grid, stream) : launch_one<D, NG, false, NT>(p, p.grid, stream);
 }
 
-// Up to eight query rows of a KV head per pass, or sixteen.
+// Up to eight query rows of a KV head per reading of the cache, or sixteen.  Sixteen of
+// 256 dims do not fit the registers: two readings measured 21.6 against 39.6 us there (4
+// x 8192 keys, two tokens of eight heads a KV head), while at d = 128 one reading takes
+// 82 against 100 us (8 x 32768 keys, 16 heads a KV head).
 template <int D, int NG>
 cudaError_t launch_rows(const Attend4Params& p, int dtype, int sms, Attend4Plan* plan, cudaStream_t stream) {
-  return p.sq * p.g <= 8 ? launch_dtype<D, NG, 1>(p, dtype, sms, plan, stream)
-                         : launch_dtype<D, NG, 2>(p, dtype, sms, plan, stream);
+  if constexpr (D <= 128) {
+    if (p.sq * p.g > 8) return launch_dtype<D, NG, 2>(p, dtype, sms, plan, stream);
+  }
+  return launch_dtype<D, NG, 1>(p, dtype, sms, plan, stream);
 }
 
 }  // namespace attend4
