@@ -473,8 +473,9 @@ typedef struct {
   int32_t max_positions;
   int32_t interleaved;            /* 0 or 1 */
   int32_t num_pages, page_size;   /* page_size: a multiple of 64 */
-  const int32_t* block_table;     /* device, [b, block_table_stride] page indices */
-  int32_t block_table_stride;
+  const int32_t* block_table;     /* device, [b, block_table_width] page indices */
+  int32_t block_table_stride;     /* entries from one sequence's row to the next (0: one row for all) */
+  int32_t block_table_width;      /* entries of a row: no sequence has more pages */
   void* k_cache;                  /* fa_kv_append: device, [num_pages, page_size, hkv, d] */
   void* v_cache;
   int64_t k_cache_strides[3];     /* (page, row, head) in elements, multiples of 8 */
@@ -532,6 +533,7 @@ typedef struct {
   int32_t num_pages, page_size;
   const int32_t* block_table;
   int32_t block_table_stride;
+  int32_t block_table_width;
   const int32_t* seqlens_k;       /* device, [b] keys per sequence */
   const int32_t* cu_seqlens;      /* device, [b + 1], or NULL */
   void* k;                        /* device, [total, hkv, d], written */
@@ -552,13 +554,13 @@ fa_status fa_kv_gather_int4(const fa_kv_gather_int4_args* args, void* stream);
  * tokens): every 16 rows (query tokens x query heads of a KV head; every 8 at d = 256)
  * read the cache once; a long chunk goes through fa_kv_gather_int4 and fa_fwd_varlen.  The cache
  * beyond a sequence's length is never used, whatever it holds.  Lengths and pages are
- * checked on the device: a sequence longer than its block-table row, or a page
- * outside [0, num_pages), is not read, FA_ERR_DEVICE_ARG is recorded and that
+ * checked on the device: a sequence longer than its block-table row or than 2^30 keys,
+ * or a page outside [0, num_pages), is not read, FA_ERR_DEVICE_ARG is recorded and that
  * sequence's O and LSE are undefined.
  */
 typedef struct {
   fa_dtype dtype;                 /* of q, o and the cache's pairs */
-  int32_t b, sq, hq, hkv, d;      /* hq % hkv == 0; d in {64, 128, 256}; b, sq, hq <= 65535 */
+  int32_t b, sq, hq, hkv, d;      /* hq % hkv == 0; d in {64, 128, 256}; b <= 65535, sq * hq / hkv <= 65536 */
   int32_t group;
   const void* q;                  /* device, [b, sq, hq, d] */
   int64_t q_strides[3];           /* (batch, row, head) in elements, multiples of 8 */
@@ -567,6 +569,7 @@ typedef struct {
   int32_t num_pages, page_size;
   const int32_t* block_table;
   int32_t block_table_stride;
+  int32_t block_table_width;
   const int32_t* seqlens_k;       /* device, [b] keys per sequence, the query tokens' own among them */
   void* o;                        /* device, [b, sq, hq, d], written */
   int64_t o_strides[3];

@@ -77,7 +77,7 @@ def _append_args(**kw):
     a.q_strides = a.q_out_strides = (8 * 128, 128)
     a.k_strides = a.v_strides = (2 * 128, 128)
     a.rotary_dim, a.max_positions = 128, 1000
-    a.num_pages, a.page_size, a.block_table_stride = 16, 64, 4
+    a.num_pages, a.page_size, a.block_table_stride, a.block_table_width = 16, 64, 4, 4
     a.k_cache_strides = a.v_cache_strides = (64 * 256, 256, 128)
     a.group = 64
     a.cache_strides = (2 * 64 * 144, 64 * 144)
@@ -90,7 +90,7 @@ BOTH = [("dtype", 2, 1), ("b", 0, 1), ("total", -1, 1), ("hq", -1, 1), ("hkv", 0
         ("total", (1 << 30) + 1, 2), ("interleaved", 2, 1), ("rotary_dim", -8, 1), ("rotary_dim", 136, 1),
         ("rotary_dim", 24, 2), ("cos_sin", 0, 1), ("cos_sin", 4100, 1), ("max_positions", 0, 1), ("num_pages", 0, 1),
         ("page_size", 0, 1), ("page_size", 96, 2), ("block_table", 0, 1), ("block_table", 4098, 1),
-        ("block_table_stride", 0, 1), ("seqlens_k", 0, 1), ("cu_seqlens", 4097, 1), ("k", 0, 1), ("v", 4104, 1),
+        ("block_table_stride", -1, 1), ("block_table_width", 0, 1), ("seqlens_k", 0, 1), ("cu_seqlens", 4097, 1), ("k", 0, 1), ("v", 4104, 1),
         ("q", 0, 1), ("q_out", 0, 1), ("q_out", 4100, 1), ("k_strides", (250, 128), 1), ("v_strides", (256, 0), 1),
         ("q_strides", (-1024, 128), 1), ("q_out_strides", (1024, 4), 1)]
 
@@ -138,7 +138,7 @@ def _gather_args(**kw):
     for f in ("cache", "block_table", "seqlens_k", "cu_seqlens", "k", "v"):
         setattr(a, f, 4096)
     a.cache_strides = (2 * 64 * 160, 64 * 160)
-    a.num_pages, a.page_size, a.block_table_stride = 16, 64, 4
+    a.num_pages, a.page_size, a.block_table_stride, a.block_table_width = 16, 64, 4, 4
     a.k_strides = a.v_strides = (256, 128)
     for k, v in kw.items():
         setattr(a, k, v)
@@ -162,7 +162,7 @@ def _attend_args(**kw):
         setattr(a, f, 4096)
     a.q_strides = a.o_strides = (8 * 128, 8 * 128, 128)
     a.cache_strides = (2 * 64 * 136, 64 * 136)
-    a.num_pages, a.page_size, a.block_table_stride = 16, 64, 4
+    a.num_pages, a.page_size, a.block_table_stride, a.block_table_width = 16, 64, 4, 4
     a.scale = 0.1
     for k, v in kw.items():
         setattr(a, k, v)
@@ -171,7 +171,7 @@ def _attend_args(**kw):
 
 @pytest.mark.parametrize("field,value,expect", [
     ("dtype", -1, 1), ("b", 0, 1), ("sq", -1, 1), ("hq", 7, 1), ("hkv", 0, 1), ("d", 96, 2), ("group", 96, 2),
-    ("b", 65536, 2), ("sq", 65536, 2), ("scale", 0.0, 1), ("scale", float("inf"), 1), ("softcap", -1.0, 1),
+    ("b", 65536, 2), ("sq", 16385, 2), ("block_table_width", 0, 1), ("scale", 0.0, 1), ("scale", float("inf"), 1), ("softcap", -1.0, 1),
     ("softcap", float("nan"), 1), ("local", 2, 1), ("cache", 4104, 1), ("page_size", 100, 2), ("seqlens_k", 0, 1),
     ("q", 0, 1), ("o", 4100, 1), ("lse", 0, 1), ("q_strides", (1024, 1024, 100), 1), ("o_strides", (1024, 0, 128), 1)])
 def test_attend_refusals(lib, field, value, expect):

@@ -289,6 +289,7 @@ class KvAppendArgs(ctypes.Structure):
         ("page_size", ctypes.c_int32),
         ("block_table", ctypes.c_void_p),
         ("block_table_stride", ctypes.c_int32),
+        ("block_table_width", ctypes.c_int32),
         ("k_cache", ctypes.c_void_p),
         ("v_cache", ctypes.c_void_p),
         ("k_cache_strides", ctypes.c_int64 * 3),
@@ -315,6 +316,7 @@ class KvGatherInt4Args(ctypes.Structure):
         ("page_size", ctypes.c_int32),
         ("block_table", ctypes.c_void_p),
         ("block_table_stride", ctypes.c_int32),
+        ("block_table_width", ctypes.c_int32),
         ("seqlens_k", ctypes.c_void_p),
         ("cu_seqlens", ctypes.c_void_p),
         ("k", ctypes.c_void_p),
@@ -343,6 +345,7 @@ class KvcacheInt4Args(ctypes.Structure):
         ("page_size", ctypes.c_int32),
         ("block_table", ctypes.c_void_p),
         ("block_table_stride", ctypes.c_int32),
+        ("block_table_width", ctypes.c_int32),
         ("seqlens_k", ctypes.c_void_p),
         ("o", ctypes.c_void_p),
         ("o_strides", ctypes.c_int64 * 3),
@@ -356,9 +359,9 @@ class KvcacheInt4Args(ctypes.Structure):
 
 # The same three structs as packers (native alignment, fields in order, arrays flat): a
 # call on a decode step's path fills one in a third of the time the mirrors take.
-KV_APPEND = struct.Struct("@6i4P8q3P3i2iPi2P6qP2qi0P")
-KV_GATHER_INT4 = struct.Struct("@6iP2q2iPi4P4q0P")
-KVCACHE_INT4 = struct.Struct("@7iP3qP2q2iPi2P3qPf2if0P")
+KV_APPEND = struct.Struct("@6i4P8q3P3i2iP2i2P6qP2qi0P")
+KV_GATHER_INT4 = struct.Struct("@6iP2q2iP2i4P4q0P")
+KVCACHE_INT4 = struct.Struct("@7iP3qP2q2iP2i2P3qPf2if0P")
 
 
 class FaError(RuntimeError):

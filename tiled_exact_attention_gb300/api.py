@@ -505,7 +505,7 @@ def _rows4(t, device: int, dtype, shape):
 
 
 def _pages(device: int, block_table, seqlens_k):
-    """(sequences, block table, its row stride, lengths) of a paged cache."""
+    """(sequences, block table, its row stride and width, lengths) of a paged cache."""
     if not isinstance(block_table, torch.Tensor) or not isinstance(seqlens_k, torch.Tensor) \
             or block_table.dtype is not torch.int32 or seqlens_k.dtype is not torch.int32 \
             or block_table.get_device() != device or seqlens_k.get_device() != device:
@@ -518,7 +518,7 @@ def _pages(device: int, block_table, seqlens_k):
     row, col = block_table.stride()
     if (col != 1 and width > 1) or (b > 1 and seqlens_k.stride(0) != 1):
         raise ValueError("block_table must be contiguous in its last dimension, seqlens_k contiguous")
-    return b, block_table.data_ptr(), row if b > 1 else width, seqlens_k.data_ptr()
+    return b, block_table.data_ptr(), row, width, seqlens_k.data_ptr()
 
 
 def _prefix(device: int, cu_seqlens, b: int, total: int) -> int:
@@ -566,7 +566,7 @@ def _append_args(device: int, k, v, block_table, seqlens_k, cu_seqlens, q, q_out
     total, hkv, d = k.shape
     k_at, k0, k1 = _rows3(k, device, dtype, total, hkv, d)
     v_at, v0, v1 = _rows3(v, device, dtype, total, hkv, d)
-    b, table, row, lens = _pages(device, block_table, seqlens_k)
+    b, table, row, width, lens = _pages(device, block_table, seqlens_k)
     cu = _prefix(device, cu_seqlens, b, total)
     hq = q_at = q0 = q1 = qo_at = qo0 = qo1 = 0
     if q is not None:
@@ -597,10 +597,10 @@ def _append_args(device: int, k, v, block_table, seqlens_k, cu_seqlens, q, q_out
         vc, vc0, vc1, vc2 = _rows4(v_cache, device, dtype, shape)
         return KV_APPEND.pack(_DT[dtype], b, total, hq, hkv, d, q_at, qo_at, k_at, v_at, q0, q1, qo0, qo1, k0, k1, v0,
                               v1, cu, lens, cs_at, rot, positions, 1 if interleaved else 0, pages, page_size, table,
-                              row, kc, vc, kc0, kc1, kc2, vc0, vc1, vc2, 0, 0, 0, 0)
+                              row, width, kc, vc, kc0, kc1, kc2, vc0, vc1, vc2, 0, 0, 0, 0)
     c, c0, c1, pages, page_size, _ = _cache4(device, cache, group, d, hkv)
     return KV_APPEND.pack(_DT[dtype], b, total, hq, hkv, d, q_at, qo_at, k_at, v_at, q0, q1, qo0, qo1, k0, k1, v0, v1,
-                          cu, lens, cs_at, rot, positions, 1 if interleaved else 0, pages, page_size, table, row, 0, 0,
+                          cu, lens, cs_at, rot, positions, 1 if interleaved else 0, pages, page_size, table, row, width, 0, 0,
                           0, 0, 0, 0, 0, 0, c, c0, c1, group)
 
 
@@ -661,10 +661,10 @@ def fa_kv_gather_int4(cache, *, group: int, block_table, seqlens_k, cu_seqlens=N
     total, hkv, d = k_out.shape
     k_at, k0, k1 = _rows3(k_out, device, dtype, total, hkv, d)
     v_at, v0, v1 = _rows3(v_out, device, dtype, total, hkv, d)
-    b, table, row, lens = _pages(device, block_table, seqlens_k)
+    b, table, row, width, lens = _pages(device, block_table, seqlens_k)
     cu = _prefix(device, cu_seqlens, b, total)
     c, c0, c1, pages, page_size, _ = _cache4(device, cache, group, d, hkv)
-    a = KV_GATHER_INT4.pack(_DT[dtype], b, total, hkv, d, group, c, c0, c1, pages, page_size, table, row, lens, cu,
+    a = KV_GATHER_INT4.pack(_DT[dtype], b, total, hkv, d, group, c, c0, c1, pages, page_size, table, row, width, lens, cu,
                             k_at, v_at, k0, k1, v0, v1)
     check(_enqueue(_lib.load().fa_kv_gather_int4, a, device, stream), "fa_kv_gather_int4")
     return k_out, v_out
@@ -697,12 +697,12 @@ def fa_fwd_kvcache_int4(q, cache, *, group: int, block_table, seqlens_k, scale=N
         q_at, q0, q2 = _rows3(q, device, dtype, b, hq, d)
         o_at, o0, o2 = _rows3(out, device, dtype, b, hq, d)
         q1 = o1 = d
-    seqs, table, row, lens = _pages(device, block_table, seqlens_k)
+    seqs, table, row, width, lens = _pages(device, block_table, seqlens_k)
     if seqs != b:
         raise ValueError("block_table must be [b, n] and seqlens_k [b]")
     c, c0, c1, pages, page_size, hkv = _cache4(device, cache, group, d, None)
     a = KVCACHE_INT4.pack(_DT[dtype], b, sq, hq, hkv, d, group, q_at, q0, q1, q2, c, c0, c1, pages, page_size, table,
-                          row, lens, o_at, o0, o1, o2, lse.data_ptr(), d ** -0.5 if scale is None else scale,
+                          row, width, lens, o_at, o0, o1, o2, lse.data_ptr(), d ** -0.5 if scale is None else scale,
                           0 if window_left is None else 1, 0 if window_left is None else window_left, softcap)
     lib = _lib.load()
     if workspace is None:

@@ -40,9 +40,13 @@ namespace attend4 {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+// The line of blocks (see the top).  Measured (us; 777 keys / 8 x 32768 / 48 uneven with
+// groups of 32 / drafted d = 64 / windowed d = 256): gap 8: 10.0 56.7 40.4 17.4 19.3; 12:
+// 9.6 56.5 41.2 16.3 19.2; 16: 9.9 56.2 41.3; items of up to 8 uncut: 11.3 56.5 40.7, of
+// up to 24: 9.9 56.4 42.5.
 constexpr int kGap = 12;            // what an item costs besides its blocks, in blocks
 constexpr int kMinShare = 4 + kGap;  // a CTA's stretch of the line at least ...
-constexpr int kUncut = 16;      // ... and items of up to so many blocks are never cut
+constexpr int kUncut = 16;          // ... and items of up to so many blocks are never cut
 constexpr int kMostParts = 32;  // CTAs that share an item at most
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -142,10 +146,11 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
   }
 }
 
-// Keys of a sequence; one that outruns its block-table row has none (and is reported).
+// Keys of a sequence; one that outruns its block-table row, or 2^30, has none (and is
+// reported).
 __device__ __forceinline__ int seq_len(const Attend4Params& p, int seq) {
   const int n = p.seqlens[seq];
-  if (n > p.bt_stride * p.page_size) {
+  if (n > p.bt_width * p.page_size || n > (1 << 30)) {
     record_error(p.status, kErrDeviceArg);
     return 0;
   }
@@ -253,6 +258,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
   using C = Cfg<D, NG, NT>;
   constexpr int J = kv4_j(D), NC = D / 32 / J, NW = D / 32, GW = NW / NG;
   constexpr int BK = C::BK, ROWS = C::ROWS;
+  // The eleven bits of an fp16 q times a code in a subnormal's lowest four bits are more
+  // than the tensor core keeps beside a larger product: LSE was off by up to 2.8e-6 of its
+  // size (in fp32).  So for fp16 all codes of K go to bits 4..7, at two more shifts a word
+  // (48 sequences, groups of 32: 41.2 to 42.3 us), which leaves 2.4e-7; bf16's eight bits
+  // lose 1.4e-6 at most and are left alone.
+  constexpr bool HIGH = !BF16;
+  constexpr float low = HIGH ? 0.0625f : 1.f;
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * C::STAGES * C::STAGE;
@@ -367,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
       batch = min(32, (pw.ue - pu + kWarps - 1) / kWarps);
       const int key = (pw.it.blo + pu + lane * kWarps) * BK, at = key / p.page_size;
       if (lane < batch) page = p.block_table[pw.it.seq * p.bt_stride + at];
-      off = pw.it.kvh * p.c_st[1] + ((key - at * p.page_size) / kKv4Unit) * C::UB;
+      off = pw.it.kvh * p.c_st[1] + static_cast<int64_t>((key - at * p.page_size) / kKv4Unit) * C::UB;
       pu += 32 * kWarps;
     }
   };
@@ -424,8 +436,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
         }
         const float s8 = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
         sum[j / GW] = j % GW == 0 ? s8 : sum[j / GW] + s8;
-        qf[j][0][nt][0] = pack_f16(x[0], x[4]);
-        qf[j][0][nt][1] = pack_f16(x[2], x[6]);
+        qf[j][0][nt][0] = pack_f16(x[0] * low, x[4] * low);
+        qf[j][0][nt][1] = pack_f16(x[2] * low, x[6] * low);
         qf[j][1][nt][0] = pack_f16(x[1] * 0.0625f, x[5] * 0.0625f);
         qf[j][1][nt][1] = pack_f16(x[3] * 0.0625f, x[7] * 0.0625f);
       }
@@ -493,11 +505,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
 #pragma unroll
             for (int j = 0; j < J; ++j) {
               const int w = c * J + j;
+              // nibbles 0, 4 (and 2, 6 through ha, hb) for the first MMA, 1, 5 (3, 7) for the second
               const uint32_t ha = wa[j] >> 8, hb = wb[j] >> 8;
+              uint32_t e0 = wa[j] & 0x000f000fu, e1 = wb[j] & 0x000f000fu, e2 = ha & 0x000f000fu, e3 = hb & 0x000f000fu;
+              if constexpr (HIGH) {
+                e0 = (wa[j] << 4) & 0x00f000f0u;
+                e1 = (wb[j] << 4) & 0x00f000f0u;
+                e2 = (wa[j] >> 4) & 0x00f000f0u;
+                e3 = (wb[j] >> 4) & 0x00f000f0u;
+              }
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                mma16816(acc[nt], wa[j] & 0x000f000fu, wb[j] & 0x000f000fu, ha & 0x000f000fu, hb & 0x000f000fu,
-                         qf[w][0][nt][0], qf[w][0][nt][1], w % GW == 0);
+                mma16816(acc[nt], e0, e1, e2, e3, qf[w][0][nt][0], qf[w][0][nt][1], w % GW == 0);
                 mma16816(acc[nt], wa[j] & 0x00f000f0u, wb[j] & 0x00f000f0u, ha & 0x00f000f0u, hb & 0x00f000f0u,
                          qf[w][1][nt][0], qf[w][1][nt][1]);
               }
@@ -595,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
           }
           top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
           if (top > 0.f && (vscale == 0.f || top * vscale > 0x1p15f)) {
-            const float now = __uint_as_float((261u - (__float_as_uint(top) >> 23)) << 23);
+            const float now = __uint_as_float((261u - max(__float_as_uint(top) >> 23, 8u)) << 23);
             if (vscale > 0.f) {
               const float a = now / vscale;
               if constexpr (C::ONES) {

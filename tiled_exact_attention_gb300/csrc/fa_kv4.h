@@ -63,7 +63,7 @@ struct KvAppendParams {
   int group;
   int num_pages, page_size;
   const int* block_table;
-  int64_t bt_stride;
+  int64_t bt_stride, bt_width;
   int* status;
 };
 
@@ -74,7 +74,7 @@ struct KvGatherParams {
   int b, total, hkv, d, group, num_pages, page_size;
   int parts;  // warps that share a token's heads
   const int* block_table;
-  int64_t bt_stride;
+  int64_t bt_stride, bt_width;
   const int* seqlens;
   const int* cu;
   void* k;
@@ -97,7 +97,7 @@ struct Attend4Params {
   int64_t c_st[2];
   int num_pages, page_size;
   const int* block_table;
-  int64_t bt_stride;
+  int64_t bt_stride, bt_width;
   const int* seqlens;
   int window_left;   // -1: no left edge
   float scale_log2;  // scale * log2(e)

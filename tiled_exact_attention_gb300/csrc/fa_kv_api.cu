@@ -29,8 +29,9 @@ bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
 bool group_ok(int group, int d) { return (group == 32 || group == 64 || group == 128) && group <= d; }
 
 // The block table and lengths of a paged cache.
-fa_status validate_pages(int num_pages, int page_size, const int32_t* table, int table_stride, const int32_t* seqlens) {
-  if (num_pages < 1 || page_size < 1 || table == nullptr || seqlens == nullptr || table_stride < 1)
+fa_status validate_pages(int num_pages, int page_size, const int32_t* table, int table_stride, int table_width,
+                         const int32_t* seqlens) {
+  if (num_pages < 1 || page_size < 1 || table == nullptr || seqlens == nullptr || table_stride < 0 || table_width < 1)
     return FA_ERR_INVALID_ARG;
   if (page_size % 64 != 0) return FA_ERR_UNSUPPORTED;
   if (!is_aligned(table, 4) || !is_aligned(seqlens, 4)) return FA_ERR_INVALID_ARG;
@@ -58,7 +59,8 @@ fa_status validate_append(const fa_kv_append_args* a, bool int4) {
     if (a->rotary_dim % (a->interleaved ? 8 : 16) != 0) return FA_ERR_UNSUPPORTED;
     if (a->cos_sin == nullptr || !is_aligned(a->cos_sin, 16) || a->max_positions < 1) return FA_ERR_INVALID_ARG;
   }
-  const fa_status v = validate_pages(a->num_pages, a->page_size, a->block_table, a->block_table_stride, a->seqlens_k);
+  const fa_status v = validate_pages(a->num_pages, a->page_size, a->block_table, a->block_table_stride, a->block_table_width,
+                                     a->seqlens_k);
   if (v != FA_OK) return v;
   if (a->cu_seqlens == nullptr ? a->total % a->b != 0 : !is_aligned(a->cu_seqlens, 4)) return FA_ERR_INVALID_ARG;
   if (int4) {
@@ -121,6 +123,7 @@ fa_status append(const fa_kv_append_args* a, bool int4, void* stream) {
   p.page_size = a->page_size;
   p.block_table = a->block_table;
   p.bt_stride = a->block_table_stride;
+  p.bt_width = a->block_table_width;
   return launch_kv_append(p, a->dtype, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -132,8 +135,9 @@ fa_status validate_attend(const fa_kvcache_int4_args* a) {
   if (!(a->softcap == 0.f || (a->softcap > 0.f && std::isfinite(a->softcap)))) return FA_ERR_INVALID_ARG;
   if ((a->local != 0 && a->local != 1) || (a->local && a->window_left < -1)) return FA_ERR_INVALID_ARG;
   if (!head_dim_ok(a->d)) return FA_ERR_UNSUPPORTED;
-  if (a->b > 65535 || a->sq > 65535 || a->hq > 65535) return FA_ERR_UNSUPPORTED;
-  const fa_status v = validate_pages(a->num_pages, a->page_size, a->block_table, a->block_table_stride, a->seqlens_k);
+  if (a->b > 65535 || static_cast<int64_t>(a->sq) * (a->hq / a->hkv) > 65536) return FA_ERR_UNSUPPORTED;
+  const fa_status v = validate_pages(a->num_pages, a->page_size, a->block_table, a->block_table_stride, a->block_table_width,
+                                     a->seqlens_k);
   if (v != FA_OK) return v;
   const fa_status c = validate_cache4(a->cache, a->cache_strides, a->page_size, a->d, a->group);
   if (c != FA_OK) return c;
@@ -171,7 +175,7 @@ bool plan_attend(const fa_kvcache_int4_args* a, int sms, AttendWork* w) {
   w->ntiles = static_cast<int>((rows + w->plan.rows - 1) / w->plan.rows);
   // no more CTAs than blocks there could be (a block table's row is the longest sequence)
   const double blocks = static_cast<double>(a->b) * a->hkv * w->ntiles *
-                        (static_cast<double>(a->block_table_stride) * a->page_size / w->plan.block + 1.0 + w->plan.gap);
+                        (static_cast<double>(a->block_table_width) * a->page_size / w->plan.block + 1.0 + w->plan.gap);
   w->grid = blocks < w->plan.max_ctas ? static_cast<int>(blocks) : w->plan.max_ctas;
   if (w->grid < 1) w->grid = 1;
   if (blocks > 2e9) return false;  // (counted in 32 bits: 2^36 keys over all KV heads and row tiles)
@@ -203,7 +207,8 @@ fa_status fa_kv_gather_int4(const fa_kv_gather_int4_args* a, void* stream) {
   if (a->b < 1 || a->total < 0 || a->hkv < 1) return FA_ERR_INVALID_ARG;
   if (!head_dim_ok(a->d)) return FA_ERR_UNSUPPORTED;
   if (a->total > (1 << 30) || a->hkv > (1 << 16)) return FA_ERR_UNSUPPORTED;
-  const fa_status v = validate_pages(a->num_pages, a->page_size, a->block_table, a->block_table_stride, a->seqlens_k);
+  const fa_status v = validate_pages(a->num_pages, a->page_size, a->block_table, a->block_table_stride, a->block_table_width,
+                                     a->seqlens_k);
   if (v != FA_OK) return v;
   const fa_status c = validate_cache4(a->cache, a->cache_strides, a->page_size, a->d, a->group);
   if (c != FA_OK) return c;
@@ -230,6 +235,7 @@ fa_status fa_kv_gather_int4(const fa_kv_gather_int4_args* a, void* stream) {
   p.page_size = a->page_size;
   p.block_table = a->block_table;
   p.bt_stride = a->block_table_stride;
+  p.bt_width = a->block_table_width;
   p.seqlens = a->seqlens_k;
   p.cu = a->cu_seqlens;
   p.k = a->k;
@@ -284,6 +290,7 @@ fa_status fa_fwd_kvcache_int4(const fa_kvcache_int4_args* a, void* workspace, si
   p.page_size = a->page_size;
   p.block_table = a->block_table;
   p.bt_stride = a->block_table_stride;
+  p.bt_width = a->block_table_width;
   p.seqlens = a->seqlens_k;
   p.window_left = a->local ? a->window_left : -1;
   p.scale_log2 = static_cast<float>(static_cast<double>(a->scale) * 1.4426950408889634);
@@ -292,7 +299,7 @@ fa_status fa_fwd_kvcache_int4(const fa_kvcache_int4_args* a, void* workspace, si
     p.sc_k = static_cast<float>(2.0 / static_cast<double>(a->softcap));
     p.sc_b = static_cast<float>(static_cast<double>(a->softcap) * 1.4426950408889634);
   }
-  p.cuts = static_cast<int64_t>(a->block_table_stride) * a->page_size > static_cast<int64_t>(w.plan.uncut) * w.plan.block;
+  p.cuts = static_cast<int64_t>(a->block_table_width) * a->page_size > static_cast<int64_t>(w.plan.uncut) * w.plan.block;
   return attend(p, a->dtype, sms, nullptr, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

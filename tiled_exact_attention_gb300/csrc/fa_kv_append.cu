@@ -135,7 +135,8 @@ struct Slot {
 // ends among the rest.
 template <int LPT>
 __device__ __forceinline__ Slot find_slot(const int* cu, int b, int total, const int* seqlens, const int* table,
-                                          int64_t bt_stride, int page_size, int num_pages, int max_positions, int tok,
+                                          int64_t bt_stride, int64_t bt_width, int page_size, int num_pages,
+                                          int max_positions, int tok,
                                           int* status) {
   Slot s{false, 0, 0, 0};
   const int lane = threadIdx.x & 31;
@@ -167,7 +168,7 @@ __device__ __forceinline__ Slot find_slot(const int* cu, int b, int total, const
   if (!live || first > tok || tok - first >= n) return s;
   const int64_t pos = static_cast<int64_t>(seqlens[seq]) - n + (tok - first);
   if (pos < 0) return s;  // padding before the sequence's first key
-  if (pos >= bt_stride * page_size || (max_positions > 0 && pos >= max_positions)) {
+  if (pos >= bt_width * page_size || (max_positions > 0 && pos >= max_positions)) {
     record_error(status, kErrDeviceArg);
     return s;
   }
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, INT4 ? 7 : 8) kv_append_kernel(const
   constexpr int U = 2;                         // rows in flight
   check_prefix(p.cu, p.b, p.total, p.status);
   const int lane = threadIdx.x & 31, k = lane % LPT;
-  const unsigned w = (blockIdx.x * kThreads + threadIdx.x) >> 5;
+  const unsigned w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int parts = p.parts, part = static_cast<int>(w % parts);  // this warp's rows: part, part + parts, ...
   const unsigned tok_u = (w / parts) * TPW + lane / LPT;
   const int tok = static_cast<int>(min(tok_u, 0x7fffffffu));
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, INT4 ? 7 : 8) kv_append_kernel(const
   const int v_first = (part + parts - (p.hq + p.hkv) % parts) % parts;
   Chunk x[U][2];
   if (part < p.hq) load_rows(x, q_at, p.q_st[1], part, p.hq, ca, cb);
-  const Slot s = find_slot<LPT>(p.cu, p.b, p.total, p.seqlens, p.block_table, p.bt_stride, p.page_size, p.num_pages,
+  const Slot s = find_slot<LPT>(p.cu, p.b, p.total, p.seqlens, p.block_table, p.bt_stride, p.bt_width, p.page_size, p.num_pages,
                                 p.rot > 0 ? p.max_positions : 0, tok, p.status);
 #pragma unroll
   for (int i = 0; i < 8; ++i) t.c[i] = t.s[i] = 0.f;
@@ -524,11 +525,11 @@ __global__ void __launch_bounds__(kThreads, 12) kv_gather4_kernel(const __grid_c
   constexpr int LPT = D / 16, TPW = 32 / LPT;
   check_prefix(p.cu, p.b, p.total, p.status);
   const int lane = threadIdx.x & 31, k = lane % LPT;
-  const unsigned w = (blockIdx.x * kThreads + threadIdx.x) >> 5;
+  const unsigned w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int parts = p.parts, part = static_cast<int>(w % parts);
   const unsigned tok_u = (w / parts) * TPW + lane / LPT;
   const int tok = static_cast<int>(min(tok_u, 0x7fffffffu));
-  const Slot s = find_slot<LPT>(p.cu, p.b, p.total, p.seqlens, p.block_table, p.bt_stride, p.page_size, p.num_pages, 0,
+  const Slot s = find_slot<LPT>(p.cu, p.b, p.total, p.seqlens, p.block_table, p.bt_stride, p.bt_width, p.page_size, p.num_pages, 0,
                                 tok, p.status);
   if (!s.ok) return;
   const int ng = D / p.group, r = s.row % kKv4Unit, chunk = cache_chunk(k, 0);
