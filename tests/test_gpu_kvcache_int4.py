@@ -45,6 +45,7 @@ CASES = {
     "drafted-wide-group": ([65, 300], 7, 10, 2, 64, 32, "fp16", 64, -1, 0.0),
     "drafted-d256": ([90, 20], 3, 16, 2, 256, 64, "bf16", 64, -1, 0.0),
     "window": ([1000, 10, 64], 1, 4, 2, 128, 64, "bf16", 64, 100, 0.0),
+    "window-all": ([300, 1], 2, 4, 2, 128, 64, "bf16", 64, (1 << 31) - 1, 0.0),
     "window-0": ([130, 1], 1, 4, 2, 64, 64, "fp16", 64, 0, 0.0),
     "window-drafted": ([700, 33, 2], 5, 8, 2, 128, 128, "fp16", 64, 37, 0.0),
     "softcap": ([500, 70], 1, 8, 2, 128, 128, "bf16", 64, -1, 5.0),

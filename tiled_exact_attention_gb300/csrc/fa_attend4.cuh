@@ -6,7 +6,8 @@
 // subnormal c 2^-24, and one whose bits are 0x00c0 is 16 c 2^-24, exactly, so a
 // 32-bit word of eight codes becomes four operand registers of m16n8k16 MMAs in
 // five integer instructions, with no conversion.  The factor 2^-24 goes into the
-// score's scale, the factor 16 into Q (exactly: powers of two).  O is likewise
+// score's scale, the factor 16 into Q (exactly: powers of two) or, for V, whose factor
+// is a row's, into O at the end.  O is likewise
 //   sum_j (p_j s_vj) (c_j - 8) + sum_j p_j (min_vj + 8 s_vj),
 // the weights p s_v rounded to fp16 for the MMA, so the rounding multiplies only the
 // centred part of V; the 8 is taken off in fp32 at the end.  (The ones that sum the
@@ -18,15 +19,23 @@
 // rows an MMA; the rows of queries (query tokens x the g query heads that share the
 // KV head) are the 8-wide N side, so few query rows waste little.  S^T leaves its MMA
 // with keys along lanes / 4 and becomes the B operand of the second product by a
-// transposing register move (movmatrix).  Each warp is a stream of its own: lane 0
-// copies whole units of the cache (K, V and their parameters are adjacent: one bulk
-// copy of some 4-10 KB) into the warp's ring in shared memory, and no barrier joins
-// the warps until the end of a (sequence, KV head, row tile).
+// transposing register move (movmatrix).  Each warp is a stream of its own: whole units
+// of the cache (K, V and their parameters are adjacent: one bulk copy of 5-10 KB) go to
+// the warp's ring in shared memory, each copied by the lane that looked its page up, and
+// no barrier joins the warps until the end of a (sequence, KV head, row tile).
 //
 // Split.  The blocks of all items (sequence, KV head, row tile) form one line that is
 // cut evenly over the grid, whatever the lengths; they are read on the device, so a
 // captured call follows them.  An item that crosses a cut is merged from fp32
 // partials by the last of its CTAs to finish.
+//
+// Bound: HBM while it streams (8 x 32768 keys of 8 heads, d = 128, groups of 128: 285 MB
+// in 46 us, 6.2 TB/s); with the start (launch, page lookup, first copies: 5 us) and the
+// joining of shares and parts at the end (5 us) the call takes 56.5 us, 5.05 TB/s, 74% of
+// the measured copy rate.  Groups of 32 cost four scales a key and need 1390 instructions
+// a block of 64 keys against 800, and are bound by their issue (48 uneven sequences: 139
+// MB in 42 us).  tcgen05 is not used: its operands come from shared memory, so the codes
+// would have to be widened into it, at four times the cache's bytes.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -109,14 +118,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   }
-}
-
-// (x, y) += a + b, in packed fp32.
-__device__ __forceinline__ void add_pair(float& x, float& y, const float* a, const float* b) {
-  asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 w, {%4, %5};\n\t"
-      "add.rn.f32x2 v, v, w;\n\tadd.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
   // to 32 blocks of an item.  Lane i holds where block i of the batch lies and copies it.
   Walk<BK, ROWS> pw = cw;
   int pu = pw.u0 + warp, batch = 0, next = 0;  // the batch after this one; blocks in it; the next to copy
-  int page = 0;
+  int page = 0, flying = 0;  // copies that have not been waited for
   int64_t off = 0;
   bool more = true;
   auto refill = [&]() {
@@ -385,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
   };
   auto copy_next = [&](int slot) {
     if (batch == 0) return;
+    ++flying;
     if (lane == next) {
       if (page < 0 || page >= p.num_pages) {
         record_error(p.status, kErrDeviceArg);
@@ -400,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
   for (int s = 0; s < C::STAGES; ++s) copy_next(s);
   int slot = 0;
   uint32_t phase = 0;
+  bool dead = false;  // a wait gave up
 
   for (bool live = true; live;) {
     const Item<BK, ROWS> it = cw.it;
@@ -481,9 +484,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
     int hold = -1;
     float vscale = 0.f;  // V's weights are held times this power of two (0: not chosen yet)
 
-    if (it.hi > it.lo)
+    if (it.hi > it.lo && !dead)
       for (int u = cw.u0 + warp; u < cw.ue; u += kWarps) {
-        mbar_wait(&full[slot], phase, p.status, kSiteFull);
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], phase, p.status, kSiteFull))) {
+          // the wait gave up (and said so): this warp reads no more, and its copies land
+          // before it leaves
+          for (; flying > 0; --flying) {
+            mbar_wait(&full[slot], phase, p.status, kSiteFull, true);
+            if (++slot == C::STAGES) {
+              slot = 0;
+              phase ^= 1u;
+            }
+          }
+          batch = 0;
+          dead = true;
+          break;
+        }
+        --flying;
         const uint8_t* st = ring + slot * C::STAGE;
         const int key0 = (it.blo + u) * BK;
         const bool edge = key0 + BK - 1 > all_hi || key0 < all_lo;
@@ -760,18 +777,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
       if (hold >= 0) {
         float* mine = reinterpret_cast<float*>(ring + hold * C::STAGE);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int j = 0; j < C::DP / 32; ++j) {
-            const int w = ps * (C::DP / 32) + j;
-            float add = tv[w / GW][nt][c];
-            if constexpr (C::ONES) add = fmaf(ones[w / GW][nt][c], -0x1p-21f * unscale, add);
-            *reinterpret_cast<float4*>(mine + (nt * 8 + 2 * t + c) * C::OP + 32 * j + 4 * g) =
-                make_float4(fmaf(o[w][0][nt][c], unscale, add), fmaf(o[w][0][nt][c + 2], unscale * 0.0625f, add),
-                            fmaf(o[w][1][nt][c], unscale, add), fmaf(o[w][1][nt][c + 2], unscale * 0.0625f, add));
-          }
+            for (int j = 0; j < C::DP / 32; ++j) {
+              const int w = ps * (C::DP / 32) + j;
+              float add = tv[w / GW][nt][c];
+              if constexpr (C::ONES) add = fmaf(ones[w / GW][nt][c], -0x1p-21f * unscale, add);
+              *reinterpret_cast<float4*>(mine + (nt * 8 + 2 * t + c) * C::OP + 32 * j + 4 * g) =
+                  make_float4(fmaf(o[w][0][nt][c], unscale, add), fmaf(o[w][0][nt][c + 2], unscale * 0.0625f, add),
+                              fmaf(o[w][1][nt][c], unscale, add), fmaf(o[w][1][nt][c + 2], unscale * 0.0625f, add));
+            }
         fence_proxy_async_smem();  // (the stage's next copy comes after these stores)
       }
       __syncthreads();

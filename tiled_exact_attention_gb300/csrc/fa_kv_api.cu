@@ -292,7 +292,8 @@ fa_status fa_fwd_kvcache_int4(const fa_kvcache_int4_args* a, void* workspace, si
   p.bt_stride = a->block_table_stride;
   p.bt_width = a->block_table_width;
   p.seqlens = a->seqlens_k;
-  p.window_left = a->local ? a->window_left : -1;
+  // (no sequence has more than 2^30 keys)
+  p.window_left = !a->local ? -1 : a->window_left < (1 << 30) ? a->window_left : 1 << 30;
   p.scale_log2 = static_cast<float>(static_cast<double>(a->scale) * 1.4426950408889634);
   if (a->softcap > 0.f) {
     // scores arrive times scale log2(e): tanh(s / c) = 1 - 2 / (2^(sc_k x) + 1), sc_b = c log2(e)
