@@ -41,6 +41,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "fa_kv4.h"
 #include "ptx.cuh"
 
@@ -904,8 +906,16 @@ cudaError_t launch_one(const Attend4Params& p, int grid, cudaStream_t stream) {
   using C = Cfg<D, NG, NT>;
   auto* k = attend4_kernel<D, NG, BF16, NT>;
   static_assert(C::SMEM <= 227 * 1024, "shared memory");
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<uint64_t> ready{0};  // devices whose kernel may use that much shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = static_cast<uint64_t>(1) << (dev & 63);
+  if ((ready.load(std::memory_order_relaxed) & bit) == 0) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   if (!p.cuts) {
     k<<<grid, kThreads, C::SMEM, stream>>>(p);
     return cudaGetLastError();
