@@ -246,6 +246,21 @@ def test_other_stream_graph_and_two_graphs():
     assert fa_sync_status() == 0
 
 
+def test_workspace_is_free_after_the_call():
+    """A call that could cut its items but cuts none leaves its workspace alone once the stream has passed it."""
+    q, cache, held, table = _problem(([900, 333], 1, 8, 2, 128, 128, "bf16", 64, -1, 0.0))
+    qg, cg, tg = q.to(DEV), torch.from_numpy(cache).to(DEV), torch.from_numpy(table).to(DEV)
+    tg = torch.nn.functional.pad(tg, (0, 64), value=1 << 29)  # a table for much longer sequences
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+    for lens in ([0, 0], [1, 3], [64, 40]):
+        n = ints(lens)
+        for _ in range(50):
+            fa_fwd_kvcache_int4(qg, cg, group=128, block_table=tg, seqlens_k=n, workspace=ws)
+            ws.fill_(0xA5)
+        assert bool((ws == 0xA5).all())
+    assert fa_sync_status() == 0
+
+
 @pytest.mark.parametrize("dt,d,group,interleaved", [("bf16", 128, 64, False), ("fp16", 64, 32, True)])
 def test_serving_run(dt, d, group, interleaved):
     """Prompts into the 4-bit cache, their attention over what the cache holds (gather + fa_fwd_varlen), a second chunk,
