@@ -160,6 +160,11 @@ __device__ __forceinline__ int seq_len(const Attend4Params& p, int seq) {
   return n > 0 ? n : 0;
 }
 
+// Rows to query tokens.
+__device__ __forceinline__ int over_g(const Attend4Params& p, int rows) {
+  return p.g_shift >= 0 ? rows >> p.g_shift : rows / p.g;
+}
+
 // One item: a row tile of one KV head of one sequence, keys [lo, hi) all in all, n
 // blocks from blo on (one, with nothing in it, where no row sees a key).
 template <int BK, int ROWS>
@@ -168,8 +173,8 @@ struct Item {
   __device__ __forceinline__ void range(const Attend4Params& p) {
     int first = len - p.sq, last = first;  // positions of the tile's first and last row
     if (p.sq > 1) {
-      first += tile * ROWS / p.g;
-      last += (min(p.sq * p.g, (tile + 1) * ROWS) - 1) / p.g;
+      first += over_g(p, tile * ROWS);
+      last += over_g(p, min(p.sq * p.g, (tile + 1) * ROWS) - 1);
     }
     hi = max(last + 1, 0);
     lo = p.window_left >= 0 ? max(0, first - p.window_left) : 0;
@@ -230,7 +235,7 @@ __device__ __forceinline__ int head_blocks(const Attend4Params& p, int seq, int*
 template <int D, bool BF16>
 __device__ __forceinline__ void store_row(const Attend4Params& p, int seq, int kvh, int row, int dim, const float* f,
                                           float inv) {
-  const int qi = p.sq > 1 ? row / p.g : 0, h = kvh * p.g + row - qi * p.g;
+  const int qi = p.sq > 1 ? over_g(p, row) : 0, h = kvh * p.g + row - qi * p.g;
   uint32_t w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -246,7 +251,7 @@ __device__ __forceinline__ void store_row(const Attend4Params& p, int seq, int k
 }
 
 __device__ __forceinline__ void store_lse(const Attend4Params& p, int seq, int kvh, int row, float M, float L) {
-  const int qi = p.sq > 1 ? row / p.g : 0, h = kvh * p.g + row - qi * p.g;
+  const int qi = p.sq > 1 ? over_g(p, row) : 0, h = kvh * p.g + row - qi * p.g;
   p.lse[(static_cast<int64_t>(seq) * p.hq + h) * p.sq + qi] = L > 0.f ? (M + lg2_approx(L)) * kLn2 : -INFINITY;
 }
 
@@ -299,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
     most = __reduce_max_sync(0xffffffffu, most);
     share = static_cast<int>((static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x);
     share = max(max(share, kMinShare), (most + kMostParts - 2) / (kMostParts - 1));
-    if (blockIdx.x > static_cast<unsigned>(total - 1) / static_cast<unsigned>(share)) return;
+    if (static_cast<int64_t>(blockIdx.x) * share >= total) return;
     const int begin = static_cast<int>(blockIdx.x) * share;
     int before = 0, rem = 0;
     for (int s0 = 0; s0 < p.b; s0 += 32) {
@@ -326,7 +331,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
     }
     cw.left = min(total - begin, share);
     cw.it.len = seq_len(p, cw.it.seq);
-    cw.it.kvh = rem / head;
+    // (a quotient below 2^16: off by one at most)
+    cw.it.kvh = static_cast<int>(__fdividef(static_cast<float>(rem), static_cast<float>(head)));
+    if (cw.it.kvh * head > rem) --cw.it.kvh;
+    if ((cw.it.kvh + 1) * head <= rem) ++cw.it.kvh;
     int u = rem - cw.it.kvh * head - kGap;  // (negative: in the gap)
     cw.it.tile = 0;
     cw.it.range(p);
@@ -355,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = cw.it.tile * ROWS + nt * 8 + g;
-      const int qi = p.sq > 1 ? r / p.g : 0, h = r - qi * p.g;
+      const int qi = p.sq > 1 ? over_g(p, r) : 0, h = r - qi * p.g;
       const uint16_t* at = static_cast<const uint16_t*>(p.q) + cw.it.seq * p.q_st[0] + qi * p.q_st[1] +
                            (cw.it.kvh * p.g + h) * p.q_st[2] + 8 * t;
 #pragma unroll
@@ -380,7 +388,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
     next = batch = 0;
     if (more) {
       batch = min(32, (pw.ue - pu + kWarps - 1) / kWarps);
-      const int key = (pw.it.blo + pu + lane * kWarps) * BK, at = key / p.page_size;
+      const int key = (pw.it.blo + pu + lane * kWarps) * BK;
+      const int at = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
       if (lane < batch) page = p.block_table[pw.it.seq * p.bt_stride + at];
       off = pw.it.kvh * p.c_st[1] + static_cast<int64_t>((key - at * p.page_size) / kKv4Unit) * C::UB;
       pu += 32 * kWarps;
@@ -453,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
         cap_rs[nt][c] = scale;
         rs[nt][c] = capped ? 1.f : scale;
         const int rc = it.tile * ROWS + nt * 8 + 2 * t + c;
-        const int pos = it.len - p.sq + (p.sq > 1 ? rc / p.g : 0);
+        const int pos = it.len - p.sq + (p.sq > 1 ? over_g(p, rc) : 0);
         row_hi[nt][c] = rc < R ? pos : -1;
         row_lo[nt][c] = p.window_left >= 0 ? pos - p.window_left : 0;
         m[nt][c] = -INFINITY;
@@ -481,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG, NT>::CTAS) attend4_kernel
     }
     // keys that every row of the tile sees: no mask there
     int all_hi = it.len - p.sq, all_lo = it.hi - 1 - p.window_left;
-    if (p.sq > 1) all_hi += it.tile * ROWS / p.g;
+    if (p.sq > 1) all_hi += over_g(p, it.tile * ROWS);
     if (p.window_left < 0) all_lo = 0;
     int hold = -1;
     float vscale = 0.f;  // V's weights are held times this power of two (0: not chosen yet)

@@ -90,6 +90,7 @@ struct Attend4Params {
   float* lse;     // [b][hq][sq]
   int64_t q_st[3], o_st[3];  // (batch, row, head) in elements
   int b, sq, hq, hkv, g, d, group;
+  int g_shift, page_shift;  // log2 of g and of page_size, -1 where they are no powers of two
   int ntiles;     // row tiles of a KV head: ceil(sq * g / rows of a tile)
   int grid;       // CTAs
   int cuts;       // 0: no item can be long enough to be cut

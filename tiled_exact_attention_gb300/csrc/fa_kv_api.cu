@@ -154,6 +154,13 @@ cudaError_t attend(const Attend4Params& p, int dtype, int sms, Attend4Plan* plan
   return attend4_d256(p, dtype, sms, plan, stream);
 }
 
+// log2 of a power of two, -1 of another number.
+int shift_of(int x) {
+  for (int i = 0; i < 31; ++i)
+    if (x == 1 << i) return i;
+  return -1;
+}
+
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // The kernel for a call, its grid and the sizes of its workspace's three parts.
@@ -268,6 +275,8 @@ fa_status fa_fwd_kvcache_int4(const fa_kvcache_int4_args* a, void* workspace, si
   p.part_ml = reinterpret_cast<float2*>(ws + w.o_bytes);
   p.counters = reinterpret_cast<int*>(ws + w.o_bytes + w.ml_bytes);
   p.ntiles = w.ntiles;
+  p.g_shift = shift_of(a->hq / a->hkv);
+  p.page_shift = shift_of(a->page_size);
   p.grid = w.grid;
   p.q = a->q;
   p.o = a->o;
