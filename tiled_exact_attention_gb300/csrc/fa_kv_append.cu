@@ -217,11 +217,13 @@ __device__ __forceinline__ void turn(Chunk (&x)[2], const Turn& t) {
   for (int q = 0; q < 2; ++q)
     if (t.on[q]) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 v = unpack2(widen2<BF16>(x[q].w[i]));
-        const float c = t.c[4 * q + i], s = t.s[4 * q + i];
-        x[q].w[i] = narrow2<BF16>(__fsub_rn(__fmul_rn(v.x, c), __fmul_rn(v.y, s)),
-                                  __fadd_rn(__fmul_rn(v.y, c), __fmul_rn(v.x, s)));
+      for (int i = 0; i < 4; i += 2) {  // two pairs: their first dims and their second ones
+        const float2 v = unpack2(widen2<BF16>(x[q].w[i])), u = unpack2(widen2<BF16>(x[q].w[i + 1]));
+        const uint64_t a = pack2(v.x, u.x), b = pack2(v.y, u.y);
+        const uint64_t c = pack2(t.c[4 * q + i], t.c[4 * q + i + 1]), s = pack2(t.s[4 * q + i], t.s[4 * q + i + 1]);
+        const float2 ya = unpack2(sub2(mul2(a, c), mul2(b, s))), yb = unpack2(add2(mul2(b, c), mul2(a, s)));
+        x[q].w[i] = narrow2<BF16>(ya.x, yb.x);
+        x[q].w[i + 1] = narrow2<BF16>(ya.y, yb.y);
       }
     }
 }
