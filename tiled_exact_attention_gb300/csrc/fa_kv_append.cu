@@ -6,11 +6,12 @@
 // lane keeps sixteen dims of one token, d / 16 lanes a token, and walks over the
 // token's heads: the rotation's cosines and sines are read once per token and stay in
 // registers, as does the token's place in the cache.  Several heads' rows are loaded
-// before the first is used.  The heads of a token are dealt to as many warps as it
-// takes to fill the GPU: one head each for a few tokens, all heads to a warp for
-// prompts.
+// before the first is used.  The heads of a token are dealt to as many warps as
+// suit the GPU: one head each for a few tokens, all heads to a warp for long prompts.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <cmath>
 
 #include "fa_kv4.h"
 #include "ptx.cuh"
@@ -19,6 +20,8 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int append_ctas(bool int4) { return int4 ? 7 : 8; }  // CTAs an SM holds
+constexpr int kGatherCtas = 12;
 
 // ---- two fp32 values in one 64-bit register, for the packed operations
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -329,7 +332,7 @@ __device__ __forceinline__ void quantise_row(const Chunk (&x)[2], int group, uin
 // for uneven chunks at d = 256; 4-bit: 60 us (5.9 TB/s) against 62.  A queue of single
 // rows ahead of the one at work was slower (69 to 80 us): loads and stores alternate then.
 template <int D, bool BF16, bool INT4>
-__global__ void __launch_bounds__(kThreads, INT4 ? 7 : 8) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
+__global__ void __launch_bounds__(kThreads, append_ctas(INT4)) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
   constexpr int LPT = D / 16, TPW = 32 / LPT;  // lanes of a token, tokens of a warp
   constexpr int U = 2;                         // rows in flight
   check_prefix(p.cu, p.b, p.total, p.status);
@@ -523,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, INT4 ? 7 : 8) kv_append_kernel(const
 // One head of a token at a time (two or four in flight measured no faster: 18 to 23 us
 // for four sequences of 4096 keys of eight heads, d = 128, at 48 warps an SM).
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads, 12) kv_gather4_kernel(const __grid_constant__ KvGatherParams p) {
+__global__ void __launch_bounds__(kThreads, kGatherCtas) kv_gather4_kernel(const __grid_constant__ KvGatherParams p) {
   constexpr int LPT = D / 16, TPW = 32 / LPT;
   check_prefix(p.cu, p.b, p.total, p.status);
   const int lane = threadIdx.x & 31, k = lane % LPT;
@@ -574,14 +577,28 @@ __global__ void __launch_bounds__(kThreads, 12) kv_gather4_kernel(const __grid_c
   }
 }
 
-// Warps that share a token's rows, and the blocks of the launch: `warps` of them where
-// there are rows enough.  (Appending four prompts of 4096 tokens, 32 / 8 heads of 128:
-// 16 warps an SM measured 73 us, 32 65 us, 64 64 us, but 64 cost the 4-bit append 6%.)
-unsigned deal(int64_t total, int rows, int d, int warps, int* parts) {
+// Warps that share a token's rows, and the blocks of the launch.  With n warps a token
+// the launch is w = groups n / resident waves of warps and lasts about
+//   (whole waves + 0.1) / w  for its last wave and the start and end of it all,
+//   times 1 + 1.5 n / rows   for the place and the angles, 1.5 rows' worth of a warp;
+// the n with the least of it is taken.  (Against a fixed 32 warps an SM, 32 / 8 heads of
+// 128, us, 16-bit and 4-bit with the gather: 1000 tokens 7.0 -> 6.6, 12.4 -> 10.7; 2500:
+// 16.2 -> 14.1, 22.3 -> 19.8; 10000: 48.4 -> 42.1, 61.7 -> 54.2; four prompts of 4096:
+// 65.3 -> 65.2, 80.3 -> 80.2; 30000: 122 -> 114, 146 -> 146.)
+unsigned deal(int64_t total, int rows, int d, int resident, int* parts) {
   const int64_t groups = (total * (d / 16) + 31) / 32;  // warps that hold the tokens once
-  int64_t n = (static_cast<int64_t>(warps) + groups - 1) / groups;
-  if (n > rows) n = rows;
-  if (n < 1) n = 1;
+  // (up to one wave more warps are better; past five there is nothing to win)
+  const int64_t one = resident / groups, least = one < 1 ? 1 : one < rows ? one : rows;
+  double best = 0.;
+  int64_t n = least;
+  for (int64_t k = least; k <= 5 * one + 5 && k <= rows; ++k) {
+    const double waves = static_cast<double>(groups * k) / resident;
+    const double cost = (std::ceil(waves) + 0.1) / waves * (1. + 1.5 * k / rows);
+    if (k == least || cost < best) {
+      best = cost;
+      n = k;
+    }
+  }
   *parts = static_cast<int>(n);
   return static_cast<unsigned>((groups * n * 32 + kThreads - 1) / kThreads);
 }
@@ -601,7 +618,7 @@ void launch_append_d(const KvAppendParams& p, int dtype, unsigned grid, cudaStre
 }  // namespace
 
 cudaError_t launch_kv_append(KvAppendParams& p, int dtype, int sms, cudaStream_t stream) {
-  const unsigned grid = deal(p.total, p.hq + 2 * p.hkv, p.d, 32 * sms, &p.parts);
+  const unsigned grid = deal(p.total, p.hq + 2 * p.hkv, p.d, kThreads / 32 * append_ctas(p.group > 0) * sms, &p.parts);
   if (p.d == 64) launch_append_d<64>(p, dtype, grid, stream);
   else if (p.d == 128) launch_append_d<128>(p, dtype, grid, stream);
   else launch_append_d<256>(p, dtype, grid, stream);
@@ -609,7 +626,7 @@ cudaError_t launch_kv_append(KvAppendParams& p, int dtype, int sms, cudaStream_t
 }
 
 cudaError_t launch_kv_gather4(KvGatherParams& p, int dtype, int sms, cudaStream_t stream) {
-  const unsigned grid = deal(p.total, p.hkv, p.d, 64 * sms, &p.parts);
+  const unsigned grid = deal(p.total, p.hkv, p.d, kThreads / 32 * kGatherCtas * sms, &p.parts);
   if (dtype == 0) {
     if (p.d == 64) kv_gather4_kernel<64, true><<<grid, kThreads, 0, stream>>>(p);
     else if (p.d == 128) kv_gather4_kernel<128, true><<<grid, kThreads, 0, stream>>>(p);
