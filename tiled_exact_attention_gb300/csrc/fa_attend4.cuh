@@ -31,7 +31,7 @@
 //
 // Bound: HBM while it streams (8 x 32768 keys of 8 heads, d = 128, groups of 128: 285 MB
 // in 46 us, 6.2 TB/s); with the start (launch, page lookup, first copies: 5 us) and the
-// joining of shares and parts at the end (5 us) the call takes 56.5 us, 5.05 TB/s, 74% of
+// joining of shares and parts at the end (5 us) the call takes 56.2 us, 5.07 TB/s, 75% of
 // the measured copy rate.  Groups of 32 cost four scales a key and need 1390 instructions
 // a block of 64 keys against 800, and are bound by their issue (48 uneven sequences: 139
 // MB in 42 us).  tcgen05 is not used: its operands come from shared memory, so the codes

@@ -20,8 +20,7 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int append_ctas(bool int4) { return int4 ? 7 : 8; }  // CTAs an SM holds
-constexpr int kGatherCtas = 12;
+constexpr int kAppendCtas = 7, kGatherCtas = 12;  // CTAs an SM holds
 
 // ---- two fp32 values in one 64-bit register, for the packed operations
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -327,12 +326,13 @@ __device__ __forceinline__ void quantise_row(const Chunk (&x)[2], int group, uin
   pair[1] = v1.pair;
 }
 
-// Two rows in flight a lane and 28 to 32 warps an SM: four rows and 20 warps measured 63
-// against 65 us (16-bit, four prompts of 4096, 6.3 TB/s of traffic) but 30 against 28 us
-// for uneven chunks at d = 256; 4-bit: 60 us (5.9 TB/s) against 62.  A queue of single
+// Two rows in flight a lane and 28 warps an SM (16-bit, four prompts of 4096: 63.6 us,
+// 6.5 TB/s of traffic; uneven chunks at d = 256: 26.6; 4-bit with the gather, prompts:
+// 80.2).  32 warps, which spill: 63.9, 27.5 and 83.2; four rows and 24 or 20 warps: 63.0,
+// 27.4 and 88.2; one row and 40 or 36 warps: 66.0, 28.0 and 86.5.  A queue of single
 // rows ahead of the one at work was slower (69 to 80 us): loads and stores alternate then.
 template <int D, bool BF16, bool INT4>
-__global__ void __launch_bounds__(kThreads, append_ctas(INT4)) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
+__global__ void __launch_bounds__(kThreads, kAppendCtas) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
   constexpr int LPT = D / 16, TPW = 32 / LPT;  // lanes of a token, tokens of a warp
   constexpr int U = 2;                         // rows in flight
   check_prefix(p.cu, p.b, p.total, p.status);
@@ -618,7 +618,7 @@ void launch_append_d(const KvAppendParams& p, int dtype, unsigned grid, cudaStre
 }  // namespace
 
 cudaError_t launch_kv_append(KvAppendParams& p, int dtype, int sms, cudaStream_t stream) {
-  const unsigned grid = deal(p.total, p.hq + 2 * p.hkv, p.d, kThreads / 32 * append_ctas(p.group > 0) * sms, &p.parts);
+  const unsigned grid = deal(p.total, p.hq + 2 * p.hkv, p.d, kThreads / 32 * kAppendCtas * sms, &p.parts);
   if (p.d == 64) launch_append_d<64>(p, dtype, grid, stream);
   else if (p.d == 128) launch_append_d<128>(p, dtype, grid, stream);
   else launch_append_d<256>(p, dtype, grid, stream);
