@@ -20,7 +20,7 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kAppendCtas = 7, kGatherCtas = 12;  // CTAs an SM holds
+constexpr int kAppendCtas = 7, kGatherCtas = 10;  // CTAs an SM holds
 
 // ---- two fp32 values in one 64-bit register, for the packed operations
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -523,8 +523,9 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) kv_append_kernel(const 
   }
 }
 
-// One head of a token at a time (two or four in flight measured no faster: 18 to 23 us
-// for four sequences of 4096 keys of eight heads, d = 128, at 48 warps an SM).
+// One head of a token at a time (two or four in flight measured no faster).  40 warps an
+// SM: four sequences of 4096 keys of eight heads, d = 128, 18.6 us, 10000 keys 12.7; 48
+// warps 19.6 and 14.3; 32 warps 18.5 and 13.7.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, kGatherCtas) kv_gather4_kernel(const __grid_constant__ KvGatherParams p) {
   constexpr int LPT = D / 16, TPW = 32 / LPT;
