@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kAppendCtas = 7, kGatherCtas = 10;  // CTAs an SM holds
+constexpr int kFlight = 2;                        // rows of the append that a warp has in flight
 
 // ---- two fp32 values in one 64-bit register, for the packed operations
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -326,15 +327,16 @@ __device__ __forceinline__ void quantise_row(const Chunk (&x)[2], int group, uin
   pair[1] = v1.pair;
 }
 
-// Two rows in flight a lane and 28 warps an SM (16-bit, four prompts of 4096: 63.6 us,
-// 6.5 TB/s of traffic; uneven chunks at d = 256: 26.6; 4-bit with the gather, prompts:
-// 80.2).  32 warps, which spill: 63.9, 27.5 and 83.2; four rows and 24 or 20 warps: 63.0,
-// 27.4 and 88.2; one row and 40 or 36 warps: 66.0, 28.0 and 86.5.  A queue of single
-// rows ahead of the one at work was slower (69 to 80 us): loads and stores alternate then.
+// Two rows in flight a lane and 28 warps an SM: 16-bit, four prompts of 4096: 62.5 us, 6.6
+// TB/s of traffic.  Other choices, before the rows were dealt as they are now (63.6 us then,
+// 26.6 for uneven chunks at d = 256, 80.2 for the prompts at 4 bits with the gather): 32
+// warps, which spill, 63.9, 27.5 and 83.2; four rows and 24 or 20 warps 63.0, 27.4 and 88.2;
+// one row and 40 or 36 warps 66.0, 28.0 and 86.5.  A queue of single rows ahead of the one
+// at work was slower (69 to 80 us): loads and stores alternate then.
 template <int D, bool BF16, bool INT4>
 __global__ void __launch_bounds__(kThreads, kAppendCtas) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
   constexpr int LPT = D / 16, TPW = 32 / LPT;  // lanes of a token, tokens of a warp
-  constexpr int U = 2;                         // rows in flight
+  constexpr int U = kFlight;
   check_prefix(p.cu, p.b, p.total, p.status);
   const int lane = threadIdx.x & 31, k = lane % LPT;
   const unsigned w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -578,26 +580,32 @@ __global__ void __launch_bounds__(kThreads, kGatherCtas) kv_gather4_kernel(const
   }
 }
 
-// Warps that share a token's rows, and the blocks of the launch.  With n warps a token
-// the launch is w = groups n / resident waves of warps and lasts about
-//   (whole waves + 0.1) / w  for its last wave and the start and end of it all,
-//   times 1 + 1.5 n / rows   for the place and the angles, 1.5 rows' worth of a warp;
-// the n with the least of it is taken.  (Against a fixed 32 warps an SM, 32 / 8 heads of
-// 128, us, 16-bit and 4-bit with the gather: 1000 tokens 7.0 -> 6.6, 12.4 -> 10.7; 2500:
-// 16.2 -> 14.1, 22.3 -> 19.8; 10000: 48.4 -> 42.1, 61.7 -> 54.2; four prompts of 4096:
-// 65.3 -> 65.2, 80.3 -> 80.2; 30000: 122 -> 114, 146 -> 146.)
-unsigned deal(int64_t total, int rows, int d, int resident, int* parts) {
+// Warps that share a token's rows (hq of one tensor, hkv of two more, `flight` at a time),
+// and the blocks of the launch.  With n warps a token the launch takes
+//   ceil(groups n / resident) + 0.25   waves of warps (the rest: its start and end)
+//   of as many rows as a warp goes through, in whole flights, + 1.3 (the token's place and
+//   angles) each;
+// the n with the least of it is taken.  Measured at 500 to 45000 tokens with 1 to 48 warps a
+// token, in three head layouts: 1 to 3% slower on average than the best n of each, where 32
+// warps an SM whatever the tokens (the n that makes them) lose 8 to 15%.  32 / 8 heads of
+// 128, 16-bit and 4-bit with the gather, us, that and this: 1000 tokens 7.0 and 6.0, 12.4
+// and 10.6; 10000: 48.4 and 41.8, 61.7 and 54.5; four prompts of 4096: 65.3 and 62.5, 80.3
+// and 79.6.
+unsigned deal(int64_t total, int d, int hq, int hkv, int flight, int resident, int* parts) {
   const int64_t groups = (total * (d / 16) + 31) / 32;  // warps that hold the tokens once
-  // (up to one wave more warps are better; past five there is nothing to win)
-  const int64_t one = resident / groups, least = one < 1 ? 1 : one < rows ? one : rows;
-  double best = 0.;
-  int64_t n = least;
-  for (int64_t k = least; k <= 5 * one + 5 && k <= rows; ++k) {
-    const double waves = static_cast<double>(groups * k) / resident;
-    const double cost = (std::ceil(waves) + 0.1) / waves * (1. + 1.5 * k / rows);
-    if (k == least || cost < best) {
-      best = cost;
-      n = k;
+  const int rows = hq + 2 * hkv;
+  int64_t n = rows;
+  if (groups * rows > resident) {
+    const int64_t most = 5 * (resident / groups) + 5;  // (past five waves there is nothing to win)
+    float best = INFINITY;
+    for (int64_t k = 1; k <= most && k <= rows; ++k) {
+      const int64_t waves = (groups * k + resident - 1) / resident, per = k * flight;
+      const int64_t flights = (hq + per - 1) / per + 2 * ((hkv + per - 1) / per);
+      const float cost = (static_cast<float>(waves) + 0.25f) * (static_cast<float>(flights * flight) + 1.3f);
+      if (cost < best) {
+        best = cost;
+        n = k;
+      }
     }
   }
   *parts = static_cast<int>(n);
@@ -619,7 +627,7 @@ void launch_append_d(const KvAppendParams& p, int dtype, unsigned grid, cudaStre
 }  // namespace
 
 cudaError_t launch_kv_append(KvAppendParams& p, int dtype, int sms, cudaStream_t stream) {
-  const unsigned grid = deal(p.total, p.hq + 2 * p.hkv, p.d, kThreads / 32 * kAppendCtas * sms, &p.parts);
+  const unsigned grid = deal(p.total, p.d, p.hq, p.hkv, kFlight, kThreads / 32 * kAppendCtas * sms, &p.parts);
   if (p.d == 64) launch_append_d<64>(p, dtype, grid, stream);
   else if (p.d == 128) launch_append_d<128>(p, dtype, grid, stream);
   else launch_append_d<256>(p, dtype, grid, stream);
@@ -627,7 +635,7 @@ cudaError_t launch_kv_append(KvAppendParams& p, int dtype, int sms, cudaStream_t
 }
 
 cudaError_t launch_kv_gather4(KvGatherParams& p, int dtype, int sms, cudaStream_t stream) {
-  const unsigned grid = deal(p.total, p.hkv, p.d, kThreads / 32 * kGatherCtas * sms, &p.parts);
+  const unsigned grid = deal(p.total, p.d, p.hkv, 0, 1, kThreads / 32 * kGatherCtas * sms, &p.parts);
   if (dtype == 0) {
     if (p.d == 64) kv_gather4_kernel<64, true><<<grid, kThreads, 0, stream>>>(p);
     else if (p.d == 128) kv_gather4_kernel<128, true><<<grid, kThreads, 0, stream>>>(p);
