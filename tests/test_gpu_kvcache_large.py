@@ -1,5 +1,6 @@
 """The paged cache's operators where offsets, lengths and tables get large or odd: caches past 4 GB, sequences past 10^5
-keys, pages that hold whole sequences, one table row for all sequences, tables that are views, two calls at once."""
+keys, pages that hold whole sequences, one table row for all sequences, tables that are views, two calls at once; and appends
+of every size in between."""
 import math
 
 import pytest
@@ -69,6 +70,40 @@ def test_long_sequence_in_one_append(dtype, d, group):
     o, lse = fa_fwd_kvcache_int4(q, cache, **kw)
     assert fa_sync_status() == 0
     _check(o[0], lse[0], _reference(q[0], k, v, group))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 16, 16), (128, 5, 3), (128, 32, 8), (256, 0, 1), (256, 7, 2)])
+def test_every_row_at_every_number_of_tokens(d, hq, hkv, interleaved):
+    """From 3 tokens, each row of which gets a warp, to 23000, whose rows are all one warp's: with a rotation that leaves
+    every row as it is (cosines 1, sines 0) every row gets to its place, in both caches and back."""
+    gen = torch.Generator(device=DEV).manual_seed(d + hq)
+    dtype, group, ps = torch.bfloat16, 64, 128
+    for n in (3, 45, 310, 777, 1200, 1900, 2600, 4100, 6001, 9500, 23000):
+        cut = n // 3
+        lens, cu = ints([cut + 5, n - cut]), ints([0, cut, n])  # the first sequence: behind five older keys
+        k, v = (_exact_rows(n, hkv, d, group, dtype, gen) for _ in range(2))
+        q = _exact_rows(n, hq, d, group, dtype, gen) if hq else None
+        width = -(-(n + 5) // ps)
+        pages = 2 * width
+        table = torch.randperm(pages, generator=gen, device=DEV).to(torch.int32).view(2, width)
+        cos_sin = torch.zeros((n + 5, 32), device=DEV)
+        cos_sin[:, :16] = 1
+        kw = dict(block_table=table, seqlens_k=lens, cu_seqlens=cu)
+        more = dict(q=q, cos_sin=cos_sin, interleaved=interleaved)
+        kc, vc = (torch.zeros((pages, ps, hkv, d), dtype=dtype, device=DEV) for _ in range(2))
+        got = fa_kv_append(k, v, kc, vc, **kw, **more)
+        assert got is None if q is None else torch.equal(got, q)
+        pos = torch.cat([torch.arange(cut, device=DEV) + 5, torch.arange(n - cut, device=DEV)])
+        seq = (torch.arange(n, device=DEV) >= cut).long()
+        page = table[seq, pos // ps].long()
+        assert torch.equal(kc[page, pos % ps], k) and torch.equal(vc[page, pos % ps], v)
+        cache = torch.zeros((pages, hkv, fa_kvcache_int4_page_bytes(ps, d, group)), dtype=torch.uint8, device=DEV)
+        got = fa_kv_append_int4(k, v, cache, group=group, **kw, **more)
+        assert got is None if q is None else torch.equal(got, q)
+        kb, vb = fa_kv_gather_int4(cache, group=group, total=n, d=d, dtype=dtype, **kw)
+        assert fa_sync_status() == 0
+        assert torch.equal(kb, k) and torch.equal(vb, v), n
 
 
 def test_caches_past_4_gb():
